@@ -382,9 +382,22 @@ class Timer:
 
 
 def exported_symbols() -> list:
-    """Names the library exports from include/tbe.h (used by host tests)."""
+    """Names the library exports from the headers in include/ (used by host tests)."""
     return ["tbe_status_str", "tbe_last_error", "tbe_select_path", "tbe_meta_capacity", "tbe_workspace_bytes",
             "tbe_forward", "tbe_preprocess", "tbe_backward_adagrad", "tbe_workspace_bytes_i64",
             "tbe_forward_i64", "tbe_backward_adagrad_i64", "tbe_backward_adagrad_noalloc",
             "tbe_probe_row_gather", "tbe_timer_create",
-            "tbe_timer_reset", "tbe_timer_read", "tbe_timer_destroy"]
+            "tbe_timer_reset", "tbe_timer_read", "tbe_timer_destroy",
+            "tbe_token_forward", "tbe_token_workspace_bytes", "tbe_token_backward",
+            "tbe_expert_workspace_bytes", "tbe_expert_plan", "tbe_expert_dispatch",
+            "tbe_expert_dispatch_backward", "tbe_expert_combine", "tbe_expert_combine_backward",
+            "tbe_distill_workspace_bytes", "tbe_distill_forward", "tbe_distill_backward",
+            "tbe_distill_step"]
+
+
+# --- language-model operators (include/tbe_lm.h) ---------------------------------------
+from .lm import (DistillDesc, ExpertDesc, ExpertPlan, TokenDesc,  # noqa: E402,F401
+                 distill_workspace, expert_workspace, tbe_distill_backward, tbe_distill_forward,
+                 tbe_distill_step, tbe_expert_combine, tbe_expert_combine_backward,
+                 tbe_expert_dispatch, tbe_expert_dispatch_backward, tbe_expert_plan,
+                 tbe_token_backward, tbe_token_forward, token_workspace)

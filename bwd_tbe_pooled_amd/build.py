@@ -27,7 +27,8 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall",
           "-I", INCLUDE, "-I", CSRC]
 
 SOURCES = ["api.cpp", "util.hip", "forward.hip", "hot_rows.hip", "sort.hip", "rle_route.hip",
-           "backward.hip", "hot_backward.hip", "probe.hip", "small_table.hip"]
+           "backward.hip", "hot_backward.hip", "probe.hip", "small_table.hip",
+           "lm_api.cpp", "token.hip", "expert.hip", "distill.hip"]
 
 
 def _compile(src: str) -> str:

@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "lm.h"
 
 namespace tbe {
 
@@ -243,15 +244,15 @@ void timer_end(tbe_timer* t, int stage, hipStream_t s) {
 
 using namespace tbe;
 
-namespace {
+static thread_local char g_last_error[256] = "";
 
-thread_local char g_last_error[256] = "";
-
-tbe_status hip_failure(hipError_t e, const char* what) {
+tbe_status tbe::hip_failure(hipError_t e, const char* what) {
   std::snprintf(g_last_error, sizeof g_last_error, "%s (%s) in %s", hipGetErrorName(e),
                 hipGetErrorString(e), what);
   return TBE_ERR_HIP;
 }
+
+namespace {
 
 #define TBE_TRY_HIP(expr)                                  \
   do {                                                     \

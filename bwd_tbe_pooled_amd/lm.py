@@ -1,0 +1,279 @@
+"""Language-model operators beside the table-batched embedding (include/tbe_lm.h).
+
+  token    tbe_token_forward, tbe_token_backward: lookup of one token table
+           with a scale, and the table's dense gradient
+  expert   tbe_expert_plan, tbe_expert_dispatch, tbe_expert_combine and their
+           backward calls: tokens sorted by expert and back with weights
+  distill  tbe_distill_forward, tbe_distill_backward, tbe_distill_step: the
+           loss against a teacher's top logits, and its gradient
+
+Argument marshalling only, as in the package's other functions. Matrices are
+2-D device tensors with unit column stride and any row stride (an output's at
+least its width); ids and per-row vectors are contiguous.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import (DTYPE_CODES, TBE_ERR_ARG, TbeError, _TORCH_W, _check, _lib, _stream)
+
+_P, _I64, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
+_IDX = {False: torch.int32, True: torch.int64}
+
+
+class tbe_token_desc(ctypes.Structure):
+    _fields_ = [("N", _I64), ("V", _I64), ("D", ctypes.c_int32), ("wdtype", ctypes.c_int),
+                ("xdtype", ctypes.c_int), ("idx64", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class tbe_expert_desc(ctypes.Structure):
+    _fields_ = [("N", _I64), ("K", ctypes.c_int32), ("E", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("dtype", ctypes.c_int), ("idx64", ctypes.c_int32)]
+
+
+class tbe_distill_desc(ctypes.Structure):
+    _fields_ = [("N", _I64), ("V", _I64), ("K", ctypes.c_int32), ("dtype", ctypes.c_int),
+                ("tdtype", ctypes.c_int), ("idx64", ctypes.c_int32),
+                ("temperature", ctypes.c_float)]
+
+
+def _declare(name, *args, restype=ctypes.c_int):
+    f = getattr(_lib, name)
+    f.restype, f.argtypes = restype, list(args)
+    return f
+
+
+# desc and stream stand first and last; m: matrix (pointer, row stride)
+_m = (_P, _I64)
+_ws = (_P, _SZ)
+_token_forward = _declare("tbe_token_forward", _P, *_m, _P, *_m, _P)
+_token_workspace_bytes = _declare("tbe_token_workspace_bytes", _P, restype=_SZ)
+_token_backward = _declare("tbe_token_backward", _P, *_m, _P, *_m, *_ws, _P)
+_expert_workspace_bytes = _declare("tbe_expert_workspace_bytes", _P, restype=_SZ)
+_expert_plan = _declare("tbe_expert_plan", _P, _P, _P, _P, _P, *_ws, _P)
+_expert_dispatch = _declare("tbe_expert_dispatch", _P, *_m, _P, *_m, _P)
+_expert_dispatch_backward = _declare("tbe_expert_dispatch_backward", _P, *_m, _P, *_m, _P)
+_expert_combine = _declare("tbe_expert_combine", _P, *_m, _P, _P, *_m, _P)
+_expert_combine_backward = _declare("tbe_expert_combine_backward", _P, *_m, *_m, _P, _P, *_m, _P, _P)
+_distill_workspace_bytes = _declare("tbe_distill_workspace_bytes", _P, restype=_SZ)
+_distill_forward = _declare("tbe_distill_forward", _P, *_m, _P, _P, _P, _P, *_ws, _P)
+_distill_backward = _declare("tbe_distill_backward", _P, *_m, _P, _P, _P, _P, *_m, _P)
+_distill_step = _declare("tbe_distill_step", _P, *_m, _P, _P, _P, _P, *_m, *_ws, _P)
+
+
+def _tensor(t, name, dtype):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if not t.is_cuda:
+        raise TypeError(f"{name}: must be a device tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+
+
+def _vec(t, name, dtype, shape):
+    """Device pointer of a contiguous tensor of this shape."""
+    _tensor(t, name, dtype)
+    if t.shape != shape:
+        raise TypeError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise TypeError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _mat(t, name, dtype, rows, cols, out=False):
+    """Device pointer and row stride of a [rows, cols] matrix."""
+    _tensor(t, name, dtype)
+    if t.shape != (rows, cols):
+        raise TypeError(f"{name}: expected shape {(rows, cols)}, got {tuple(t.shape)}")
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise TypeError(f"{name}: columns must be contiguous")
+    if rows <= 1:
+        ld = cols
+    elif out and ld < cols:
+        raise TypeError(f"{name}: rows of an output must not overlap")
+    return t.data_ptr(), ld
+
+
+def _scratch(ws):
+    if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
+        raise TypeError("workspace: expected a contiguous device tensor")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _workspace(bytes_of, desc, where, device):
+    n = int(bytes_of(desc.ref))
+    if n == 0:
+        raise TbeError(TBE_ERR_ARG, where)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+class _LmDesc:
+    """Owns the C description `c`; `ref` is its address."""
+
+    def _own(self, c, idx64):
+        self.c = c
+        self.ref = ctypes.addressof(c)
+        self.idx = _IDX[bool(idx64)]
+
+
+# --- token table -------------------------------------------------------------------
+class TokenDesc(_LmDesc):
+    """N tokens of a table of V rows and D columns. wdtype: type of the table
+    and its gradient, xdtype: of the rows looked up and their gradient."""
+
+    def __init__(self, N: int, V: int, D: int, wdtype: str = "bf16", xdtype: str = "bf16",
+                 idx64: bool = True, scale: float = 1.0):
+        self.N, self.V, self.D = int(N), int(V), int(D)
+        self.w, self.x = _TORCH_W[wdtype], _TORCH_W[xdtype]
+        self._own(tbe_token_desc(self.N, self.V, self.D, DTYPE_CODES[wdtype], DTYPE_CODES[xdtype],
+                                 int(bool(idx64)), float(scale)), idx64)
+
+
+def token_workspace(desc: TokenDesc, device="cuda"):
+    """Workspace of tbe_token_backward."""
+    return _workspace(_token_workspace_bytes, desc, "tbe_token_workspace_bytes", device)
+
+
+def tbe_token_forward(desc: TokenDesc, W, ids, out, stream=None):
+    """out[n] = scale * W[ids[n]]; zeros where the id is outside [0, V)."""
+    N, D = desc.N, desc.D
+    _check(_token_forward(desc.ref, *_mat(W, "W", desc.w, desc.V, D),
+                          _vec(ids, "ids", desc.idx, (N,)),
+                          *_mat(out, "out", desc.x, N, D, True), _stream(stream)),
+           "tbe_token_forward")
+
+
+def tbe_token_backward(desc: TokenDesc, g, ids, gW, ws, stream=None):
+    """gW[v] = scale * sum of g[n] over the tokens with ids[n] = v, all V rows."""
+    N, D = desc.N, desc.D
+    _check(_token_backward(desc.ref, *_mat(g, "g", desc.x, N, D),
+                           _vec(ids, "ids", desc.idx, (N,)),
+                           *_mat(gW, "gW", desc.w, desc.V, D, True), *_scratch(ws),
+                           _stream(stream)), "tbe_token_backward")
+
+
+# --- experts -----------------------------------------------------------------------
+class ExpertDesc(_LmDesc):
+    """N tokens with K assignments each to E experts, rows of D columns."""
+
+    def __init__(self, N: int, K: int, E: int, D: int, dtype: str = "bf16", idx64: bool = True):
+        self.N, self.K, self.E, self.D = int(N), int(K), int(E), int(D)
+        self.M = self.N * self.K
+        self.x = _TORCH_W[dtype]
+        self._own(tbe_expert_desc(self.N, self.K, self.E, self.D, DTYPE_CODES[dtype],
+                                  int(bool(idx64))), idx64)
+
+
+class ExpertPlan:
+    """Device buffers of a plan: `offsets` [E+1], `order` [N*K], `slots` [N*K]."""
+
+    def __init__(self, desc: ExpertDesc, device="cuda"):
+        self.offsets = torch.empty(desc.E + 1, dtype=torch.int32, device=device)
+        self.order = torch.empty(desc.M, dtype=torch.int32, device=device)
+        self.slots = torch.empty(desc.M, dtype=torch.int32, device=device)
+
+
+def expert_workspace(desc: ExpertDesc, device="cuda"):
+    """Workspace of tbe_expert_plan."""
+    return _workspace(_expert_workspace_bytes, desc, "tbe_expert_workspace_bytes", device)
+
+
+def tbe_expert_plan(desc: ExpertDesc, ids, plan: ExpertPlan, ws, stream=None):
+    """Sorts the assignments by expert into `plan` (dropped ones at the end)."""
+    i32, M = torch.int32, desc.M
+    _check(_expert_plan(desc.ref, _vec(ids, "ids", desc.idx, (desc.N, desc.K)),
+                        _vec(plan.offsets, "plan.offsets", i32, (desc.E + 1,)),
+                        _vec(plan.order, "plan.order", i32, (M,)),
+                        _vec(plan.slots, "plan.slots", i32, (M,)), *_scratch(ws),
+                        _stream(stream)), "tbe_expert_plan")
+
+
+def tbe_expert_dispatch(desc: ExpertDesc, x, slots, xs, stream=None):
+    """xs[place of (n, k)] = x[n]; zeros at the places of dropped assignments."""
+    _check(_expert_dispatch(desc.ref, *_mat(x, "x", desc.x, desc.N, desc.D),
+                            _vec(slots, "slots", torch.int32, (desc.M,)),
+                            *_mat(xs, "xs", desc.x, desc.M, desc.D, True), _stream(stream)),
+           "tbe_expert_dispatch")
+
+
+def tbe_expert_dispatch_backward(desc: ExpertDesc, dxs, slots, dx, stream=None):
+    """dx[n] = sum over kept k of dxs[place of (n, k)]."""
+    _check(_expert_dispatch_backward(desc.ref, *_mat(dxs, "dxs", desc.x, desc.M, desc.D),
+                                     _vec(slots, "slots", torch.int32, (desc.M,)),
+                                     *_mat(dx, "dx", desc.x, desc.N, desc.D, True),
+                                     _stream(stream)), "tbe_expert_dispatch_backward")
+
+
+def tbe_expert_combine(desc: ExpertDesc, ys, slots, w, out, stream=None):
+    """out[n] = sum over kept k of w[n, k] * ys[place of (n, k)]."""
+    _check(_expert_combine(desc.ref, *_mat(ys, "ys", desc.x, desc.M, desc.D),
+                           _vec(slots, "slots", torch.int32, (desc.M,)),
+                           _vec(w, "w", torch.float32, (desc.N, desc.K)),
+                           *_mat(out, "out", desc.x, desc.N, desc.D, True), _stream(stream)),
+           "tbe_expert_combine")
+
+
+def tbe_expert_combine_backward(desc: ExpertDesc, dout, ys, slots, w, dys, dw, stream=None):
+    """dys[place of (n, k)] = w[n, k] * dout[n], dw[n, k] = <dout[n], ys[place]>;
+    zeros where the assignment is dropped. dys may be ys."""
+    N, K, D, M = desc.N, desc.K, desc.D, desc.M
+    _check(_expert_combine_backward(desc.ref, *_mat(dout, "dout", desc.x, N, D),
+                                    *_mat(ys, "ys", desc.x, M, D),
+                                    _vec(slots, "slots", torch.int32, (M,)),
+                                    _vec(w, "w", torch.float32, (N, K)),
+                                    *_mat(dys, "dys", desc.x, M, D, True),
+                                    _vec(dw, "dw", torch.float32, (N, K)), _stream(stream)),
+           "tbe_expert_combine_backward")
+
+
+# --- distillation --------------------------------------------------------------------
+class DistillDesc(_LmDesc):
+    """N rows of V logits (dtype) against K teacher's logits a row (tdtype)."""
+
+    def __init__(self, N: int, V: int, K: int, dtype: str = "bf16", tdtype: str = "f32",
+                 idx64: bool = True, temperature: float = 1.0):
+        self.N, self.V, self.K = int(N), int(V), int(K)
+        self.x, self.t = _TORCH_W[dtype], _TORCH_W[tdtype]
+        self._own(tbe_distill_desc(self.N, self.V, self.K, DTYPE_CODES[dtype], DTYPE_CODES[tdtype],
+                                   int(bool(idx64)), float(temperature)), idx64)
+
+
+def distill_workspace(desc: DistillDesc, device="cuda"):
+    """Workspace of tbe_distill_forward and tbe_distill_step."""
+    return _workspace(_distill_workspace_bytes, desc, "tbe_distill_workspace_bytes", device)
+
+
+def tbe_distill_forward(desc: DistillDesc, x, ids, t, loss, stats, ws, stream=None):
+    """loss[n] = tau^2 KL(teacher || student) of row n; stats [N, 2] for the backward."""
+    N, K = desc.N, desc.K
+    _check(_distill_forward(desc.ref, *_mat(x, "x", desc.x, N, desc.V),
+                            _vec(ids, "ids", desc.idx, (N, K)), _vec(t, "t", desc.t, (N, K)),
+                            _vec(loss, "loss", torch.float32, (N,)),
+                            _vec(stats, "stats", torch.float32, (N, 2)), *_scratch(ws),
+                            _stream(stream)), "tbe_distill_forward")
+
+
+def tbe_distill_backward(desc: DistillDesc, x, ids, t, stats, gl, gx, stream=None):
+    """gx = gl * tau * (softmax(x / tau) - teacher). gx may be x."""
+    N, K, V = desc.N, desc.K, desc.V
+    _check(_distill_backward(desc.ref, *_mat(x, "x", desc.x, N, V),
+                             _vec(ids, "ids", desc.idx, (N, K)), _vec(t, "t", desc.t, (N, K)),
+                             _vec(stats, "stats", torch.float32, (N, 2)),
+                             _vec(gl, "gl", torch.float32, (N,)),
+                             *_mat(gx, "gx", desc.x, N, V, True), _stream(stream)),
+           "tbe_distill_backward")
+
+
+def tbe_distill_step(desc: DistillDesc, x, ids, t, gl, loss, gx, ws, stream=None):
+    """Loss and gradient in one call. gx may be x."""
+    N, K, V = desc.N, desc.K, desc.V
+    _check(_distill_step(desc.ref, *_mat(x, "x", desc.x, N, V),
+                         _vec(ids, "ids", desc.idx, (N, K)), _vec(t, "t", desc.t, (N, K)),
+                         _vec(gl, "gl", torch.float32, (N,)),
+                         _vec(loss, "loss", torch.float32, (N,)),
+                         *_mat(gx, "gx", desc.x, N, V, True), *_scratch(ws), _stream(stream)),
+           "tbe_distill_step")
