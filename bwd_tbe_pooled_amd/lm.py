@@ -65,6 +65,7 @@ _distill_step = _declare("tbe_distill_step", _P, *_m, _P, _P, _P, _P, *_m, *_ws,
 
 
 def _tensor(t, name, dtype):
+    """Raises for what is not a device tensor of this type."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if not t.is_cuda:
@@ -75,7 +76,8 @@ def _tensor(t, name, dtype):
 
 def _vec(t, name, dtype, shape):
     """Device pointer of a contiguous tensor of this shape."""
-    _tensor(t, name, dtype)
+    if type(t) is not torch.Tensor or t.dtype is not dtype or not t.is_cuda:
+        _tensor(t, name, dtype)
     if t.shape != shape:
         raise TypeError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
@@ -85,7 +87,8 @@ def _vec(t, name, dtype, shape):
 
 def _mat(t, name, dtype, rows, cols, out=False):
     """Device pointer and row stride of a [rows, cols] matrix."""
-    _tensor(t, name, dtype)
+    if type(t) is not torch.Tensor or t.dtype is not dtype or not t.is_cuda:
+        _tensor(t, name, dtype)
     if t.shape != (rows, cols):
         raise TypeError(f"{name}: expected shape {(rows, cols)}, got {tuple(t.shape)}")
     ld, unit = t.stride()
@@ -101,7 +104,7 @@ def _mat(t, name, dtype, rows, cols, out=False):
 def _scratch(ws):
     if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
         raise TypeError("workspace: expected a contiguous device tensor")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.nbytes
 
 
 def _workspace(bytes_of, desc, where, device):
