@@ -21,7 +21,7 @@ constexpr int64_t kTokenMaxRows = int64_t(kSplitBins - 1) * kBucketIds;
 struct SplitShape {
   int32_t tiles, len;
 };
-SplitShape split_shape(int64_t n);
+SplitShape split_shape(int64_t n, int32_t bins);
 
 // Stable split of M assignments by expert (expert.hip's plan).
 // counts: int32[tiles * stride(E + 1)], unused with one tile.
@@ -45,12 +45,14 @@ struct TokenLayout {
   int32_t chunk;      // sorted places per wave of the sum
   int64_t chunks;
   int64_t part_ld;    // floats per partial row
-  bool filtered;      // one launch sorts (few tokens)
+  bool few;           // no sort, one launch (few tokens)
+  bool filtered;      // one launch sorts
   size_t off;         // int32[V + 1]: first sorted place of each id
-  size_t pos, sid;    // int32[N]: token and id at each sorted place
-  size_t lpos, llow;  // int32[N]: the same before the sort inside buckets
+  size_t sorted;      // int2[N]: token and id (top bit: of a run longer than a chunk) at each sorted place
+  size_t split;       // int2[N]: token and lower part of the id, before the sort inside buckets
   size_t bstart;      // int32[buckets + 1]
   size_t counts;      // split counts
+  size_t listed;      // long runs: int32[4], of which 2 counts; int4[2][chunks]
   size_t parts;       // float[chunks][2][part_ld]
   size_t total;
 };

@@ -46,7 +46,7 @@ tbe_status check(const tbe_distill_desc* d) {
 }
 
 size_t expert_bytes(const tbe_expert_desc& d) {
-  const SplitShape sh = split_shape(d.N * d.K);
+  const SplitShape sh = split_shape(d.N * d.K, d.E + 1);
   const size_t counts = sh.tiles > 1 ? sizeof(int32_t) * (size_t)sh.tiles * split_stride(d.E + 1) : 0;
   return counts + 256;
 }

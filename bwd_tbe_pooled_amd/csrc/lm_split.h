@@ -60,34 +60,64 @@ __device__ __forceinline__ uint64_t lanes_below() {
   return (uint64_t(1) << lane_id()) - 1;
 }
 
+constexpr int kSplitRounds = 8;  // rounds of 64 keys a wave has in registers
+
+// A wave's keys of up to kSplitRounds rounds from j0 (key.load(j), or
+// key.none() from `end` on): all loads are in flight together.
+template <typename Key>
+__device__ __forceinline__ void load_keys(const Key& key, int64_t j0, int64_t end, int step,
+                                          typename Key::type (&k)[kSplitRounds]) {
+#pragma unroll
+  for (int q = 0; q < kSplitRounds; ++q) {
+    const int64_t j = j0 + (int64_t)q * step + lane_id();
+    k[q] = j < end ? key.load(j) : key.none();
+  }
+}
+
 // counts[tile * stride + bin] of the tile this workgroup owns.
-template <typename BinOf>
+template <typename Key>
 __device__ void split_count(int64_t n, SplitShape sh, int32_t bins, int32_t stride,
-                            int32_t* __restrict__ counts, BinOf bin_of) {
+                            int32_t* __restrict__ counts, const Key& key) {
   __shared__ int32_t hist[kSplitBins];
   const int32_t tile = blockIdx.x;
-  for (int i = threadIdx.x; i < bins; i += kSplitThreads) hist[i] = 0;
-  __syncthreads();
   const int64_t a = (int64_t)tile * sh.len;
   const int64_t e = a + sh.len < n ? a + sh.len : n;
-  for (int64_t j = a + threadIdx.x; j < e; j += kSplitThreads)
-    __hip_atomic_fetch_add(&hist[bin_of(j)], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+  for (int i = threadIdx.x; i < bins; i += kSplitThreads) hist[i] = 0;
+  __syncthreads();
+  for (int64_t j0 = a + wave_index() * kWave; j0 < e; j0 += kSplitRounds * kSplitThreads) {
+    typename Key::type k[kSplitRounds];
+    load_keys(key, j0, e, kSplitThreads, k);
+#pragma unroll
+    for (int q = 0; q < kSplitRounds; ++q)
+      if (j0 + q * kSplitThreads + lane_id() < e)
+        __hip_atomic_fetch_add(&hist[key.bin(k[q])], 1, __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_WORKGROUP);
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < stride; i += kSplitThreads)
     counts[(int64_t)tile * stride + i] = i < bins ? hist[i] : 0;
 }
 
-// Calls place(j, bin, p) for every key of this workgroup's tile: p is the
+// Calls place(j, key, bin, p) for every key of this workgroup's tile: p is the
 // place of key j in the stable order. Fills s.start (valid after the call in
 // every thread).
-template <typename BinOf, typename Place>
+template <typename Key, typename Place>
 __device__ void split_tile(int64_t n, SplitShape sh, int32_t bins, int bits, int32_t stride,
-                           const int32_t* __restrict__ counts, SplitLds& s, BinOf bin_of,
+                           const int32_t* __restrict__ counts, SplitLds& s, const Key& key,
                            Place place) {
   const int tid = threadIdx.x;
   const int wave = wave_index();
   const int lane = lane_id();
   const int32_t tile = blockIdx.x;
+  // this tile's keys, a span of whole rounds of 64 per wave
+  const int64_t a = (int64_t)tile * sh.len;
+  const int64_t e = a + sh.len < n ? a + sh.len : n;
+  const int32_t span = sh.len / kSplitWaves;
+  const int64_t wa = a + (int64_t)wave * span;
+  const int64_t we = wa + span < e ? wa + span : e;
+  typename Key::type k[kSplitRounds];
+  load_keys(key, wa, we, kWave, k);  // of a short span all, of a long one the first batch
+
   if (tid < bins) {
 #pragma unroll
     for (int w = 0; w < kSplitWaves; ++w) s.wave[w][tid] = 0;
@@ -120,15 +150,14 @@ __device__ void split_tile(int64_t n, SplitShape sh, int32_t bins, int bits, int
     }
   }
 
-  // this tile's keys, a span of whole rounds of 64 per wave
-  const int64_t a = (int64_t)tile * sh.len;
-  const int64_t e = a + sh.len < n ? a + sh.len : n;
-  const int32_t span = sh.len / kSplitWaves;
-  const int64_t wa = a + (int64_t)wave * span;
-  const int64_t we = wa + span < e ? wa + span : e;
-  for (int64_t j = wa + lane; j < we; j += kWave)
-    __hip_atomic_fetch_add(&s.wave[wave][bin_of(j)], 1, __ATOMIC_RELAXED,
-                           __HIP_MEMORY_SCOPE_WORKGROUP);
+  for (int64_t j0 = wa; j0 < we; j0 += kSplitRounds * kWave) {
+    if (j0 != wa) load_keys(key, j0, we, kWave, k);
+#pragma unroll
+    for (int q = 0; q < kSplitRounds; ++q)
+      if (j0 + q * kWave + lane < we)
+        __hip_atomic_fetch_add(&s.wave[wave][key.bin(k[q])], 1, __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_WORKGROUP);
+  }
   __syncthreads();
 
   int32_t tot = 0;
@@ -154,18 +183,23 @@ __device__ void split_tile(int64_t n, SplitShape sh, int32_t bins, int bits, int
   __syncthreads();
 
   const uint64_t below = lanes_below();
-  for (int64_t j0 = wa; j0 < we; j0 += kWave) {
-    const int64_t j = j0 + lane;
-    const bool ok = j < we;
-    const int32_t bin = ok ? bin_of(j) : 0;
-    const uint64_t m = same_bin((uint32_t)bin, ok, bits);
-    if (ok) {
-      const int32_t p = s.wave[wave][bin] + __popcll(m & below);
-      place(j, bin, p);
+  for (int64_t j0 = wa; j0 < we; j0 += kSplitRounds * kWave) {
+    if (span > kSplitRounds * kWave) load_keys(key, j0, we, kWave, k);
+#pragma unroll
+    for (int q = 0; q < kSplitRounds; ++q) {
+      const int64_t j = j0 + q * kWave + lane;
+      if (j - lane >= we) break;
+      const bool ok = j < we;
+      const int32_t bin = ok ? key.bin(k[q]) : 0;
+      const uint64_t m = same_bin((uint32_t)bin, ok, bits);
+      if (ok) {
+        const int32_t p = s.wave[wave][bin] + __popcll(m & below);
+        place(j, k[q], bin, p);
+      }
+      wave_lds_sync();  // every lane has read its bin's next place
+      if (ok && (m & below) == 0) s.wave[wave][bin] += __popcll(m);
+      wave_lds_sync();
     }
-    wave_lds_sync();  // every lane has read its bin's next place
-    if (ok && (m & below) == 0) s.wave[wave][bin] += __popcll(m);
-    wave_lds_sync();
   }
 }
 

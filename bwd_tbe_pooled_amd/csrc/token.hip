@@ -56,12 +56,17 @@ __global__ __launch_bounds__(256) void token_forward_kernel(
 
 // --- sort -----------------------------------------------------------------------
 struct BucketOf {
+  using type = int32_t;
   const void* ids;
   int32_t idx64, shift, buckets;
-  int64_t V;
-  __device__ __forceinline__ int32_t operator()(int64_t j) const {
+  int32_t V;
+  __device__ __forceinline__ type none() const { return -1; }
+  __device__ __forceinline__ type load(int64_t j) const {  // -1: padding
     const int64_t v = load_id(ids, idx64, j);
-    return v >= 0 && v < V ? (int32_t)(v >> shift) : buckets;  // padding: the last bin
+    return v >= 0 && v < V ? (int32_t)v : -1;
+  }
+  __device__ __forceinline__ int32_t bin(type v) const {
+    return v >= 0 ? v >> shift : buckets;  // padding: the last bin
   }
 };
 
@@ -72,205 +77,310 @@ __global__ __launch_bounds__(kSplitThreads) void token_count_kernel(
 
 __global__ __launch_bounds__(kSplitThreads) void token_split_kernel(
     BucketOf of, int64_t N, SplitShape sh, int bits, int32_t stride,
-    const int32_t* __restrict__ counts, int32_t* __restrict__ bstart, int32_t* __restrict__ lpos,
-    int32_t* __restrict__ llow) {
+    const int32_t* __restrict__ counts, int32_t* __restrict__ bstart, int2* __restrict__ split) {
   __shared__ SplitLds s;
   const int32_t low = (1 << of.shift) - 1;
   split_tile(N, sh, of.buckets + 1, bits, stride, counts, s, of,
-             [&](int64_t j, int32_t bin, int32_t p) {
+             [&](int64_t j, int32_t v, int32_t bin, int32_t p) {
                if (bin == of.buckets) return;
-               lpos[p] = (int32_t)j;
-               llow[p] = (int32_t)load_id(of.ids, of.idx64, j) & low;
+               split[p] = make_int2((int32_t)j, v & low);
              });
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i <= of.buckets; i += kSplitThreads) bstart[i] = s.start[i];
 }
 
-constexpr int kBucketThreads = 512;
-constexpr int kBucketWaves = kBucketThreads / kWave;
-constexpr int kFilterTokens = 8192;      // tokens a workgroup filters by itself
+constexpr int kFilterTokens = 4096;      // tokens a workgroup filters by itself
+constexpr int kRounds = 8;               // rounds of 64 places a wave has in flight
 
-// Sorts one bucket by the lower part of the id: sorted places pos/sid, and
-// off[v] of the bucket's ids. FILTER: the bucket's tokens are picked out of
-// all ids into LDS first.
-template <bool FILTER>
-__global__ __launch_bounds__(kBucketThreads) void token_bucket_kernel(
-    BucketOf of, int32_t N, const int32_t* __restrict__ bstart, const int32_t* __restrict__ lpos,
-    const int32_t* __restrict__ llow, int32_t* __restrict__ off, int32_t* __restrict__ pos,
-    int32_t* __restrict__ sid) {
+// Sorts one bucket by the lower part of the id: (token, id) at the sorted
+// places, the id's top bit marking runs longer than `chunk`, and off[v] of the
+// bucket's ids.
+// FILTER: the bucket's tokens are picked out of all ids into LDS first.
+template <int THREADS, bool FILTER>
+__global__ __launch_bounds__(THREADS) void token_bucket_kernel(
+    BucketOf of, int32_t N, int32_t chunk, const int32_t* __restrict__ bstart,
+    const int2* __restrict__ split, int32_t* __restrict__ off, int2* __restrict__ sorted,
+    int32_t* __restrict__ listed) {
+  constexpr int kWaves = THREADS / kWave;
   extern __shared__ int32_t lds[];
   int32_t* const next = lds;  // [wave][low]: counts, then the next place
-  int32_t* const list = lds + (kBucketWaves << of.shift);  // FILTER: pos | low << 13
-  __shared__ int32_t sums[2 * kBucketWaves];
+  const int shift = of.shift;
+  const int32_t width = 1 << shift;
+  uint32_t* const is_long = reinterpret_cast<uint32_t*>(lds + (kWaves << shift));  // [low]
+  int32_t* const list = lds + ((kWaves + 1) << shift);  // FILTER: pos | low << 12
+  __shared__ int32_t sums[2 * kWaves];
   const int tid = threadIdx.x;
   const int wave = wave_index();
   const int lane = lane_id();
   const int32_t b = blockIdx.x;
-  const int shift = of.shift;
-  const int32_t width = 1 << shift;
   const uint64_t below = lanes_below();
   int32_t base = 0, n = 0;
+  if (b == 0 && tid < 2) listed[tid] = 0;  // the sum's lists of long runs
 
   if constexpr (FILTER) {
     // the wave's span of tokens: those of this bucket and of lower ones
-    const int32_t span = ((N + kBucketThreads - 1) / kBucketThreads) * kWave;
+    static_assert(kFilterTokens <= kRounds * THREADS || !FILTER, "a span is kRounds rounds");
+    const int32_t span = ((N + THREADS - 1) / THREADS) * kWave;
     const int32_t wa = wave * span;
     const int32_t we = wa + span < N ? wa + span : N;
+    int32_t id[kRounds];
+#pragma unroll
+    for (int q = 0; q < kRounds; ++q) {
+      const int32_t j = wa + q * kWave + lane;
+      id[q] = j < we ? of.load(j) : of.none();
+    }
     int32_t mine = 0, lower = 0;
-    for (int32_t j0 = wa; j0 < we; j0 += kWave) {
-      const int32_t bin = j0 + lane < we ? of(j0 + lane) : of.buckets;
+#pragma unroll
+    for (int q = 0; q < kRounds; ++q) {
+      const int32_t bin = of.bin(id[q]);
       mine += __popcll(__ballot(bin == b));
       lower += __popcll(__ballot(bin < b));
     }
     if (lane == 0) {
       sums[wave] = mine;
-      sums[kBucketWaves + wave] = lower;
+      sums[kWaves + wave] = lower;
     }
     __syncthreads();
     int32_t at = 0;
 #pragma unroll
-    for (int w = 0; w < kBucketWaves; ++w) {
+    for (int w = 0; w < kWaves; ++w) {
       at += w < wave ? sums[w] : 0;
       n += sums[w];
-      base += sums[kBucketWaves + w];
+      base += sums[kWaves + w];
     }
-    for (int32_t j0 = wa; j0 < we; j0 += kWave) {
-      const int32_t j = j0 + lane;
-      const bool ok = j < we && of(j) == b;
-      const uint64_t m = __ballot(ok);
-      if (ok)
-        list[at + __popcll(m & below)] =
-            j | (((int32_t)load_id(of.ids, of.idx64, j) & (width - 1)) << 13);
-      at += __popcll(m);
+    if (mine) {
+#pragma unroll
+      for (int q = 0; q < kRounds; ++q) {
+        const bool ok = of.bin(id[q]) == b;
+        const uint64_t m = __ballot(ok);
+        if (ok)
+          list[at + __popcll(m & below)] =
+              (wa + q * kWave + lane) | ((id[q] & (width - 1)) << 12);
+        at += __popcll(m);
+      }
     }
   } else {
     base = bstart[b];
     n = bstart[b + 1] - base;
   }
-  auto low_of = [&](int32_t i) { return FILTER ? list[i] >> 13 : llow[base + i]; };
-  auto pos_of = [&](int32_t i) { return FILTER ? list[i] & (kFilterTokens - 1) : lpos[base + i]; };
+  auto token_of = [&](int32_t i) {
+    return FILTER ? make_int2(list[i] & (kFilterTokens - 1), list[i] >> 12) : split[base + i];
+  };
 
-  for (int i = tid; i < kBucketWaves * width; i += kBucketThreads) next[i] = 0;
+  for (int i = tid; i < (kWaves << shift); i += THREADS) next[i] = 0;
   __syncthreads();
-  const int32_t span = ((n + kBucketThreads - 1) / kBucketThreads) * kWave;
+  const int32_t span = ((n + THREADS - 1) / THREADS) * kWave;
   const int32_t wa = wave * span;
   const int32_t we = wa + span < n ? wa + span : n;
-  for (int32_t i = wa + lane; i < we; i += kWave)
-    __hip_atomic_fetch_add(&next[(wave << shift) + low_of(i)], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+  int2 tok[kRounds];  // (token, low) of the batch in hand, low -1 past the end
+  auto load_batch = [&](int32_t i0) {
+#pragma unroll
+    for (int q = 0; q < kRounds; ++q) {
+      const int32_t i = i0 + q * kWave + lane;
+      tok[q] = i < we ? token_of(i) : make_int2(0, -1);
+    }
+  };
+  for (int32_t i0 = wa; i0 < we; i0 += kRounds * kWave) {
+    load_batch(i0);
+#pragma unroll
+    for (int q = 0; q < kRounds; ++q) {
+      // one lane adds for all lanes of its id: a frequent id would take the
+      // counter 64 times a round
+      if (i0 + q * kWave >= we) break;
+      const bool ok = tok[q].y >= 0;
+      const uint64_t m = same_bin((uint32_t)tok[q].y, ok, shift);
+      if (ok && (m & below) == 0)
+        __hip_atomic_fetch_add(&next[(wave << shift) + tok[q].y], __popcll(m), __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_WORKGROUP);
+    }
+  }
   __syncthreads();
 
   // exclusive scan over the ids of the bucket; each thread has `per` of them
-  const int32_t per = (width + kBucketThreads - 1) / kBucketThreads;
+  const int32_t per = (width + THREADS - 1) / THREADS;
   int32_t mine = 0;
   for (int32_t q = 0; q < per; ++q) {
     const int32_t l = tid * per + q;
-    if (l < width)
-      for (int w = 0; w < kBucketWaves; ++w) mine += next[(w << shift) + l];
+    if (l < width) {
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) mine += next[(w << shift) + l];
+    }
   }
   const int32_t inc = wave_inclusive_scan(mine);
   if (lane == kWave - 1) sums[wave] = inc;
   __syncthreads();
   int32_t run = base + inc - mine;
 #pragma unroll
-  for (int w = 0; w < kBucketWaves; ++w) run += w < wave ? sums[w] : 0;
+  for (int w = 0; w < kWaves; ++w) run += w < wave ? sums[w] : 0;
   for (int32_t q = 0; q < per; ++q) {
     const int32_t l = tid * per + q;
     if (l >= width) break;
-    const int64_t v = ((int64_t)b << shift) + l;
+    const int32_t v = (b << shift) + l;
     if (v <= of.V) off[v] = run;
-    for (int w = 0; w < kBucketWaves; ++w) {
+    const int32_t first = run;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
       const int32_t c = next[(w << shift) + l];
       next[(w << shift) + l] = run;
       run += c;
     }
+    is_long[l] = run - first > chunk ? 0x80000000u : 0u;
   }
   // the table's end, where it is the end of a bucket
-  if (b == of.buckets - 1 && tid == 0 && ((int64_t)of.buckets << shift) == of.V) off[of.V] = base + n;
+  if (b == of.buckets - 1 && tid == 0 && (of.buckets << shift) == of.V) off[of.V] = base + n;
   __syncthreads();
 
-  for (int32_t i0 = wa; i0 < we; i0 += kWave) {
-    const int32_t i = i0 + lane;
-    const bool ok = i < we;
-    const int32_t low = ok ? low_of(i) : 0;
-    const uint64_t m = same_bin((uint32_t)low, ok, shift);
-    if (ok) {
-      const int32_t p = next[(wave << shift) + low] + __popcll(m & below);
-      pos[p] = pos_of(i);
-      sid[p] = (b << shift) + low;
+  for (int32_t i0 = wa; i0 < we; i0 += kRounds * kWave) {
+    if (span > kRounds * kWave) load_batch(i0);
+#pragma unroll
+    for (int q = 0; q < kRounds; ++q) {
+      if (i0 + q * kWave >= we) break;
+      const bool ok = tok[q].y >= 0;
+      const int32_t l = ok ? tok[q].y : 0;
+      const uint64_t m = same_bin((uint32_t)l, ok, shift);
+      if (ok) {
+        const int32_t p = next[(wave << shift) + l] + __popcll(m & below);
+        sorted[p] = make_int2(tok[q].x, (int32_t)((uint32_t)((b << shift) + l) | is_long[l]));
+      }
+      wave_lds_sync();
+      if (ok && (m & below) == 0) next[(wave << shift) + l] += __popcll(m);
+      wave_lds_sync();
     }
-    wave_lds_sync();
-    if (ok && (m & below) == 0) next[(wave << shift) + low] += __popcll(m);
-    wave_lds_sync();
   }
 }
 
 // --- sum -----------------------------------------------------------------------
-constexpr int kZeroRows = 16;   // table rows a wave looks at for empty ones
+constexpr int kMaxChunk = 32;      // a wave's places and the window around them fit its lanes
+constexpr int kZeroVectors = 4;    // vectors of zeros per thread
+constexpr int kWavePieces = 32;    // pieces of a run one wave joins alone, at most
+
+// Runs longer than a chunk, (id, first chunk, pieces) in any order: each is joined by
+// itself. list[0..capacity): up to kWavePieces pieces, list[capacity..): more.
+struct LongRuns {
+  int32_t* count;  // [2]
+  int4* list;
+  int32_t capacity;
+};
+
+// Zeros of the table's empty rows, in spans of 1024 vectors (a row taken as nz
+// of them), one per workgroup: stores in the order of addresses from many short
+// workgroups fill memory fastest here (1 GiB at 6.0 TB/s; with 64 KB per
+// workgroup 5.5, from a grid that strides over the table 4.4). It has to stay
+// short: with whole lines of a dense table instead, and the test of a vector's
+// second row that this takes, the sum kernel's 1.2 GB went from 6.0 to 4.7 TB/s.
+template <typename WT, int VZ>
+struct EmptySpans {
+  WT* gW;
+  int64_t ldgw;
+  int32_t V, D;
+
+  EmptySpans(void* table, int64_t ld, const tbe_token_desc& d)
+      : gW(static_cast<WT*>(table)), ldgw(ld), V((int32_t)d.V), D(d.D) {}
+  unsigned blocks() const {
+    const int64_t vectors = (int64_t)V * ((D + VZ - 1) / VZ);
+    return (unsigned)((vectors + kSpan - 1) / kSpan);
+  }
+  static constexpr int kSpan = 256 * kZeroVectors;
+  static constexpr int kRows = kSpan + 1;  // rows a span touches, at most
+
+  // First row of a span, and which of its vectors the span starts with.
+  __device__ __forceinline__ int64_t first_row(uint32_t block, uint32_t* rem) const {
+    const uint32_t nz = (uint32_t)((D + VZ - 1) / VZ);
+    const uint64_t first = (uint64_t)block * kSpan;
+    const int64_t row = first >> 32 ? (int64_t)(first / nz) : (int64_t)((uint32_t)first / nz);
+    *rem = (uint32_t)(first - (uint64_t)row * nz);
+    return row;
+  }
+
+  // has(r): whether row row0 + r has tokens.
+  template <typename Has>
+  __device__ __forceinline__ void write(int64_t row0, uint32_t rem, Has has) const {
+    const uint32_t nz = (uint32_t)((D + VZ - 1) / VZ);
+    typename Pack<WT, VZ>::raw zero;
+    zero_raw(zero);
+    bool empty[kZeroVectors];
+    WT* to[kZeroVectors];
+#pragma unroll
+    for (int i = 0; i < kZeroVectors; ++i) {
+      const uint32_t o = rem + i * 256 + threadIdx.x;
+      const uint32_t r = o / nz;
+      const bool in = row0 + r < V;
+      empty[i] = !has(in ? r : 0) && in;
+      to[i] = gW + (row0 + r) * ldgw + pack_column<VZ>((int32_t)(o - r * nz), D);
+    }
+#pragma unroll
+    for (int i = 0; i < kZeroVectors; ++i)
+      if (empty[i]) store_pack<WT, VZ>(to[i], zero);
+  }
+};
 
 // VE: columns per lane of the sums (16 bytes of g), VZ: of the zero rows.
 template <typename WT, typename XT, int VE, int VZ>
 __global__ __launch_bounds__(256) void token_sum_kernel(
     const XT* __restrict__ g, int64_t ldg, const int32_t* __restrict__ off,
-    const int32_t* __restrict__ pos, const int32_t* __restrict__ sid, int32_t V, int32_t D,
-    float scale, WT* __restrict__ gW, int64_t ldgw, float* __restrict__ parts, int64_t part_ld,
-    int32_t chunk, Units units, uint32_t sum_blocks) {
+    const int2* __restrict__ sorted, int32_t V, int32_t D,
+    float scale, WT* __restrict__ gW, int64_t ldgw, LongRuns runs,
+    float* __restrict__ parts, int64_t part_ld, int32_t chunk, Units units, uint32_t sum_blocks,
+    EmptySpans<WT, VZ> empty) {
   using RX = typename Pack<XT, VE>::raw;
-  const int lane = lane_id();
-  const int32_t nv = (D + VE - 1) / VE;
-
-  if (blockIdx.x >= sum_blocks) {  // zero rows
-    const int32_t v0 = ((int32_t)(blockIdx.x - sum_blocks) * 4 + wave_index()) * kZeroRows;
-    const int32_t v = v0 + lane;
-    const bool empty = lane < kZeroRows && v < V && off[v] == off[v + 1];
-    uint64_t m = __ballot(empty);
-    typename Pack<WT, VZ>::raw zero;
-    zero_raw(zero);
-    const int32_t nz = (D + VZ - 1) / VZ;
-    while (m) {
-      const int r = __builtin_ctzll(m);
-      m &= m - 1;
-      WT* row = gW + (int64_t)(v0 + r) * ldgw;
-      for (int32_t i = lane; i < nz; i += kWave)
-        store_pack_once<WT, VZ>(row + pack_column<VZ>(i, D), zero);
-    }
+  if (blockIdx.x >= sum_blocks) {
+    uint32_t rem;
+    const int64_t row0 = empty.first_row(blockIdx.x - sum_blocks, &rem);
+    empty.write(row0, rem, [&](uint32_t r) { return off[row0 + r] != off[row0 + r + 1]; });
     return;
   }
-
+  const int lane = lane_id();
+  const int32_t nv = (D + VE - 1) / VE;
   const int32_t kept = off[V];
   for (UnitWalk u(units, blockIdx.x * 4 + wave_index()); u.valid(units); u.next(units)) {
     const int64_t b64 = u.row * chunk;
     if (b64 >= kept) continue;
     const int32_t b = (int32_t)b64;
-    const int32_t e = kept - b > chunk ? b + chunk : kept;
+    const int32_t n = kept - b > chunk ? chunk : kept - b;
     const int32_t i = u.seg * kWave + lane;
     const bool in = i < nv;
     const int32_t col = in ? pack_column<VE>(i, D) : 0;
     const XT* gc = g + col;
     float* part = parts + (u.row * 2) * part_ld + col;
 
-    // leading places of a run that began before this chunk: its short rest
-    // belongs to the wave of its start, a long run's piece to this one
-    int32_t s0 = b;
-    bool head = false;
-    {
-      const int32_t v = sid[b];
-      const int32_t r0 = off[v], r1 = off[v + 1];
-      if (r0 < b) {
-        if (r1 - r0 > chunk) head = true;
-        else s0 = r1;
-      }
+    // lane l has place b - 1 + l
+    const int32_t k = b - 1 + lane;
+    const bool there = k >= 0 && k < kept;
+    const int32_t at = there ? k : b;
+    const int32_t w = sorted[at].y, p = sorted[at].x;
+    const int32_t before = __shfl_up(w, 1);
+    // first places of runs among lanes 1.. (lane 0 only tells where lane 1's run began)
+    const uint64_t firsts =
+        __ballot(there && lane > 0 && (k == 0 || before != w)) |
+        (kept - b + 1 < kWave ? uint64_t(1) << (kept - b + 1) : 0);  // the end of all places
+    const uint64_t longs = __ballot(there && w < 0);
+    const uint64_t mine = (uint64_t(2) << n) - 2;      // lanes 1..n
+    int32_t s0 = 1, s1 = n + 1;
+    bool head = false, tail = false;
+    if (!(firsts & 2)) {
+      if (longs & 2) head = true;                      // a piece of a long run
+      else s0 = __builtin_ctzll(firsts);               // a short run: its start's chunk sums it
     }
-    // the last run that starts here, if it crosses the border: whole if short
-    int32_t s1 = e;
-    bool tail = false;
-    if (e < kept) {
-      const int32_t v = sid[e - 1];
-      const int32_t r0 = off[v], r1 = off[v + 1];
-      if (r0 >= b && r1 > e) {
-        if (r1 - r0 > chunk) tail = true;
-        else s1 = r1;
+    if (firsts & mine) {
+      const int last = 63 - __builtin_clzll(firsts & mine);
+      if ((longs >> last) & 1) {
+        tail = true;                                   // goes on in the next chunk
+      } else {
+        const uint64_t after = firsts & ~((uint64_t(2) << last) - 1);
+        s1 = after ? __builtin_ctzll(after) : kWave;
       }
+    } else if (!head) {
+      s0 = s1;
     }
+    if (tail && u.seg == 0 && lane == 0) {
+      // a long run starts here: into the list for one wave, or for 16, to join
+      const int32_t v = sorted[b + n - 1].y & 0x7fffffff;
+      const int32_t pieces = (off[v + 1] - 1) / chunk - (int32_t)u.row + 1;
+      const int hot = pieces > kWavePieces;
+      runs.list[hot * runs.capacity + atomicAdd(runs.count + hot, 1)] =
+          make_int4(v, (int32_t)u.row, pieces, 0);
+    }
+
     float acc[VE];
 #pragma unroll
     for (int q = 0; q < VE; ++q) acc[q] = 0.f;
@@ -280,29 +390,31 @@ __global__ __launch_bounds__(256) void token_sum_kernel(
 #pragma unroll
       for (int q = 0; q < KU; ++q) {
         zero_raw(r[q]);
-        if (k0 + q < s1 && in) r[q] = load_pack_once<XT, VE>(gc + (int64_t)pos[k0 + q] * ldg);
+        if (k0 + q < s1) {
+          const int32_t row = __builtin_amdgcn_readlane(p, k0 + q);
+          if (in) r[q] = load_pack_once<XT, VE>(gc + (int64_t)row * ldg);
+        }
       }
 #pragma unroll
       for (int q = 0; q < KU; ++q) {
-        const int32_t k = k0 + q;
-        if (k >= s1) break;
+        if (k0 + q >= s1) break;
         float f[VE];
         widen<XT, VE>(r[q], f);
 #pragma unroll
         for (int j = 0; j < VE; ++j) acc[j] += f[j];
-        const int32_t v = sid[k];
-        const bool last = k + 1 == s1;
-        if (!last && sid[k + 1] == v) continue;
+        const bool last = k0 + q + 1 == s1;
+        if (!last && !((firsts >> (k0 + q + 1)) & 1)) continue;
         // the run ends here: a whole one goes to the table, a piece of a
         // long one to this chunk's partial rows
         if (in) {
           if (head || (last && tail)) {
             store_pack<float, VE>(part + (head ? 0 : part_ld), narrow<float, VE>(acc));
           } else {
+            const int32_t v = __builtin_amdgcn_readlane(w, k0 + q);
             float o[VE];
 #pragma unroll
             for (int j = 0; j < VE; ++j) o[j] = acc[j] * scale;
-            store_pack_once<WT, VE>(gW + (int64_t)v * ldgw + col, narrow<WT, VE>(o));
+            store_pack<WT, VE>(gW + (int64_t)v * ldgw + col, narrow<WT, VE>(o));
           }
         }
         head = false;
@@ -313,53 +425,172 @@ __global__ __launch_bounds__(256) void token_sum_kernel(
   }
 }
 
-// The run that starts in chunk c and has more than `chunk` tokens: its piece
-// in c's second partial row and its pieces in the first rows of the chunks
-// after it. 4 groups of 256 threads share the pieces, 4 columns per thread.
-template <typename WT>
-__global__ __launch_bounds__(1024) void token_join_kernel(
-    const int32_t* __restrict__ off, const int32_t* __restrict__ sid, int32_t V, int32_t D,
-    float scale, WT* __restrict__ gW, int64_t ldgw, const float* __restrict__ parts,
-    int64_t part_ld, int32_t chunk, int64_t chunks) {
-  __shared__ float4 red[3][256];
-  const int32_t kept = off[V];
-  const int group = threadIdx.x / 256;
-  const int t = threadIdx.x % 256;
-  for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const int64_t e = (c + 1) * chunk;
-    if (e >= kept) return;
-    const int32_t v = sid[e - 1];
-    const int32_t r0 = off[v], r1 = off[v + 1];
-    if (r0 < c * chunk || r1 <= e || r1 - r0 <= chunk) continue;
-    const int64_t pieces = (r1 - 1) / chunk - c;  // after the first one
-    for (int32_t d0 = (blockIdx.y * 256 + t) * 4; d0 - t * 4 < D; d0 += gridDim.y * 1024) {
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (d0 < D) {
-        // piece 0 is the run's first; rows are padded to whole float4s
+// The sum of a long run's pieces p = p0, p0 + step, ... in 4 columns from d:
+// its first piece is in the second partial row of chunk c, the others in the
+// first rows of the chunks after it. (Partial rows are padded to float4s.)
+__device__ __forceinline__ float4 sum_pieces(const float* __restrict__ parts, int64_t part_ld,
+                                             int64_t c, int32_t p0, int32_t step, int32_t pieces,
+                                             int64_t d) {
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-        for (int64_t p = group; p <= pieces; p += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(
-              parts + ((c + p) * 2 + (p == 0 ? 1 : 0)) * part_ld + d0);
-          a.x += f.x; a.y += f.y; a.z += f.z; a.w += f.w;
-        }
-      }
-      if (group) red[group - 1][t] = a;
-      __syncthreads();
-      if (group == 0 && d0 < D) {
+  for (int32_t p = p0; p < pieces; p += step) {
+    const float4 f = *reinterpret_cast<const float4*>(
+        parts + ((c + p) * 2 + (p == 0 ? 1 : 0)) * part_ld + d);
+    a.x += f.x; a.y += f.y; a.z += f.z; a.w += f.w;
+  }
+  return a;
+}
+
+// Joins the long runs, 256 columns at a time: a wave per run of few pieces, a
+// workgroup's 16 waves together on one of many.
+constexpr int kJoinWaves = 16;
+constexpr int kJoinBlocks = 512;
+
+template <typename WT>
+__global__ __launch_bounds__(kJoinWaves * kWave) void token_join_kernel(
+    LongRuns runs, int32_t D, float scale, WT* __restrict__ gW, int64_t ldgw,
+    const float* __restrict__ parts, int64_t part_ld) {
+  __shared__ float4 red[kJoinWaves][kWave];
+  const int wave = wave_index();
+  const int lane = lane_id();
+  const int32_t panels = (D + 255) / 256;
+  const int64_t few = (int64_t)runs.count[0] * panels, many = (int64_t)runs.count[1] * panels;
+  for (int64_t i = blockIdx.x; i < many; i += gridDim.x) {
+    const int4 run = runs.list[runs.capacity + i / panels];
+    const int64_t d = (i % panels) * 256 + lane * 4;
+    red[wave][lane] = d < D ? sum_pieces(parts, part_ld, run.y, wave, kJoinWaves, run.z, d)
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();
+    const int64_t col = (i % panels) * 256 + threadIdx.x;
+    if (threadIdx.x < 256 && col < D) {
+      float t = 0.f;
 #pragma unroll
-        for (int q = 0; q < 3; ++q) {
-          const float4 f = red[q][t];
-          a.x += f.x; a.y += f.y; a.z += f.z; a.w += f.w;
-        }
-        const float o[4] = {a.x, a.y, a.z, a.w};
-        WT* row = gW + (int64_t)v * ldgw;
+      for (int q = 0; q < kJoinWaves; ++q) t += reinterpret_cast<const float*>(red[q])[threadIdx.x];
+      gW[run.x * ldgw + col] = round_to<WT>(t * scale);
+    }
+    __syncthreads();
+  }
+  // neighbouring waves in different workgroups: few units go to all CUs
+  for (int64_t i = (int64_t)wave * gridDim.x + blockIdx.x; i < few; i += gridDim.x * kJoinWaves) {
+    const int4 run = runs.list[i / panels];
+    const int64_t d = (i % panels) * 256 + lane * 4;
+    if (d >= D) continue;
+    const float4 a = sum_pieces(parts, part_ld, run.y, 0, 1, run.z, d);
+    const float o[4] = {a.x, a.y, a.z, a.w};
+    WT* row = gW + run.x * ldgw;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (d0 + q < D) row[d0 + q] = round_to<WT>(o[q] * scale);
-      }
-      __syncthreads();
+    for (int q = 0; q < 4; ++q)
+      if (d + q < D) row[d + q] = round_to<WT>(o[q] * scale);
+  }
+}
+
+// --- few tokens --------------------------------------------------------------------
+// One launch without a sort. A workgroup of the first kind has one token and a
+// segment of columns; the first token of an id sums the rows of all tokens of
+// that id, a quarter of them per wave, the others leave. One of the second
+// kind writes zeros over 1024 vectors of the table, but for rows that have a
+// token. Each finds its tokens by looking at all ids, 4 a thread at most: that
+// is cheaper than the three launches of the sort.
+constexpr int kFewTokens = 1024;
+constexpr int kFewIds = kFewTokens / 256;  // ids per thread
+
+template <typename WT, typename XT, int VE, int VZ>
+__global__ __launch_bounds__(256) void token_few_kernel(
+    const XT* __restrict__ g, int64_t ldg, BucketOf of, int32_t N, int32_t D, float scale,
+    WT* __restrict__ gW, int64_t ldgw, int32_t segs, uint32_t sum_blocks,
+    EmptySpans<WT, VZ> empty) {
+  using RX = typename Pack<XT, VE>::raw;
+  constexpr int kUsedWords = (EmptySpans<WT, VZ>::kRows + 31) / 32;  // a bit per row
+  __shared__ union {
+    struct {
+      float part[3][kWave][VE];
+      int32_t token[kFewTokens];
+      int32_t count[kFewIds * 4];
+    } s;
+    uint32_t used[kUsedWords];
+  } l;
+  const int tid = threadIdx.x, lane = lane_id(), wave = wave_index();
+  int32_t id[kFewIds];  // of token q * 256 + tid
+#pragma unroll
+  for (int q = 0; q < kFewIds; ++q) id[q] = q * 256 + tid < N ? of.load(q * 256 + tid) : of.none();
+
+  if (blockIdx.x >= sum_blocks) {
+    uint32_t rem;
+    const int64_t row0 = empty.first_row(blockIdx.x - sum_blocks, &rem);
+    if (tid < kUsedWords) l.used[tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kFewIds; ++q) {
+      const int64_t r = id[q] - row0;
+      if (id[q] >= 0 && r >= 0 && r < 32 * kUsedWords) atomicOr(&l.used[r / 32], 1u << (r % 32));
+    }
+    __syncthreads();
+    empty.write(row0, rem, [&](uint32_t r) { return (l.used[r / 32] >> (r % 32)) & 1; });
+    return;
+  }
+
+  const int32_t n = (int32_t)(blockIdx.x / (uint32_t)segs), seg = (int32_t)(blockIdx.x % (uint32_t)segs);
+  const int32_t v = of.load(n);
+  if (v < 0) return;
+  bool earlier = false;
+  uint64_t mine[kFewIds];
+#pragma unroll
+  for (int q = 0; q < kFewIds; ++q) {
+    earlier |= id[q] == v && q * 256 + tid < n;
+    mine[q] = __ballot(id[q] == v);
+    if (lane == 0) l.s.count[q * 4 + wave] = __popcll(mine[q]);
+  }
+  if (__syncthreads_or(earlier)) return;
+  int32_t m = 0, at[kFewIds];
+#pragma unroll
+  for (int i = 0; i < kFewIds * 4; ++i) {
+    if (i % 4 == wave) at[i / 4] = m;
+    m += l.s.count[i];
+  }
+#pragma unroll
+  for (int q = 0; q < kFewIds; ++q)
+    if (id[q] == v) l.s.token[at[q] + __popcll(mine[q] & lanes_below())] = q * 256 + tid;
+  __syncthreads();
+
+  const int32_t i = seg * kWave + lane;
+  const bool in = i < (D + VE - 1) / VE;
+  const int32_t col = in ? pack_column<VE>(i, D) : 0;
+  const int32_t each = (m + 3) / 4;
+  const int32_t k1 = (wave + 1) * each < m ? (wave + 1) * each : m;
+  float acc[VE];
+#pragma unroll
+  for (int e = 0; e < VE; ++e) acc[e] = 0.f;
+  constexpr int KU = 8;  // rows in flight
+  for (int32_t k0 = wave * each; k0 < k1; k0 += KU) {
+    RX r[KU];
+#pragma unroll
+    for (int q = 0; q < KU; ++q) {
+      zero_raw(r[q]);
+      if (k0 + q < k1 && in) r[q] = load_pack_once<XT, VE>(g + l.s.token[k0 + q] * ldg + col);
+    }
+#pragma unroll
+    for (int q = 0; q < KU; ++q) {
+      float f[VE];
+      widen<XT, VE>(r[q], f);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) acc[e] += f[e];
     }
   }
+  if (m > 1) {
+    if (wave)
+#pragma unroll
+      for (int e = 0; e < VE; ++e) l.s.part[wave - 1][lane][e] = acc[e];
+    __syncthreads();
+    if (wave) return;
+#pragma unroll
+    for (int w = 0; w < 3; ++w)
+#pragma unroll
+      for (int e = 0; e < VE; ++e) acc[e] += l.s.part[w][lane][e];
+  }
+  if (wave || !in) return;
+#pragma unroll
+  for (int e = 0; e < VE; ++e) acc[e] *= scale;
+  store_pack<WT, VE>(gW + v * ldgw + col, narrow<WT, VE>(acc));
 }
 
 template <typename WT, typename XT, typename F>
@@ -367,6 +598,20 @@ hipError_t with_width(int32_t D, F f) {
   constexpr int VE = pack_elems<WT, XT>();
   if (D >= VE) return f(std::integral_constant<int, VE>{});
   return f(std::integral_constant<int, 1>{});
+}
+
+// f(element of gW, element of g, columns per lane of the sums, of the zeros)
+template <typename F>
+hipError_t with_gradient_types(const tbe_token_desc& d, F f) {
+  return with_type(d.wdtype, [&](auto wt) {
+    return with_type(d.xdtype, [&](auto xt) {
+      using std::integral_constant;
+      if (d.D >= 8)
+        return f(wt, xt, integral_constant<int, pack_elems<decltype(xt)>()>{},
+                 integral_constant<int, pack_elems<decltype(wt)>()>{});
+      return f(wt, xt, integral_constant<int, 1>{}, integral_constant<int, 1>{});
+    });
+  });
 }
 
 int bits_for(int32_t bins) {
@@ -383,10 +628,11 @@ TokenLayout token_layout(const tbe_token_desc& d) {
   while (((d.V - 1) >> L.shift) + 1 > kSplitBins - 1) ++L.shift;
   L.buckets = (int32_t)(((d.V - 1) >> L.shift) + 1);
   L.filtered = d.N <= kFilterTokens;
-  // 64 sorted places a wave, fewer where that leaves the chip without waves
+  // 32 sorted places a wave, 16 where that leaves the chip without waves
   const int32_t vec = d.xdtype == TBE_F32 ? 4 : 8;
   const int64_t segs = (d.D + 64 * vec - 1) / (64 * vec);
-  L.chunk = d.N * segs >= 64 * 2048 ? 64 : 16;
+  L.few = d.N <= kFewTokens && d.N * segs <= 8 * kFewTokens;
+  L.chunk = d.N * segs >= kMaxChunk * 2048 ? kMaxChunk : 16;
   L.chunks = (d.N + L.chunk - 1) / L.chunk;
   L.part_ld = ((int64_t)d.D + 3) / 4 * 4;
   size_t at = 0;
@@ -395,16 +641,15 @@ TokenLayout token_layout(const tbe_token_desc& d) {
     at += (bytes + 255) & ~size_t(255);
     return a;
   };
-  const size_t n4 = sizeof(int32_t) * (size_t)d.N;
+  const size_t n8 = sizeof(int2) * (size_t)d.N;
   L.off = take(sizeof(int32_t) * ((size_t)d.V + 1));
-  L.pos = take(n4);
-  L.sid = take(n4);
+  L.sorted = take(n8);
   if (!L.filtered) {
-    L.lpos = take(n4);
-    L.llow = take(n4);
+    L.split = take(n8);
     L.bstart = take(sizeof(int32_t) * ((size_t)L.buckets + 1));
-    L.counts = take(sizeof(int32_t) * (size_t)split_shape(d.N).tiles * split_stride(L.buckets + 1));
+    L.counts = take(sizeof(int32_t) * (size_t)split_shape(d.N, L.buckets + 1).tiles * split_stride(L.buckets + 1));
   }
+  L.listed = take(sizeof(int4) * (1 + 2 * (size_t)L.chunks));
   L.parts = take(sizeof(float) * 2 * (size_t)L.chunks * (size_t)L.part_ld);
   L.total = at;
   return L;
@@ -435,55 +680,66 @@ hipError_t launch_token_backward(const tbe_token_desc& d, const TokenLayout& L, 
                                  hipStream_t s) {
   char* base = static_cast<char*>(ws);
   auto at = [&](size_t o) { return reinterpret_cast<int32_t*>(base + o); };
-  int32_t *off = at(L.off), *pos = at(L.pos), *sid = at(L.sid);
+  int32_t *off = at(L.off), *listed = at(L.listed);
+  int2 *sorted = reinterpret_cast<int2*>(base + L.sorted), *split = reinterpret_cast<int2*>(base + L.split);
+  const LongRuns runs{listed, reinterpret_cast<int4*>(listed + 4), (int32_t)L.chunks};
   float* parts = reinterpret_cast<float*>(base + L.parts);
-  const BucketOf of{ids, d.idx64, L.shift, L.buckets, d.V};
-  const size_t lds = sizeof(int32_t) * ((size_t)kBucketWaves << L.shift);
+  const BucketOf of{ids, d.idx64, L.shift, L.buckets, (int32_t)d.V};
+  if (L.few) {
+    return with_gradient_types(d, [&](auto wt, auto xt, auto ve, auto vz) {
+      using WT = decltype(wt);
+      using XT = decltype(xt);
+      constexpr int VE = decltype(ve)::value, VZ = decltype(vz)::value;
+      const int32_t segs = (d.D + kWave * VE - 1) / (kWave * VE);
+      const unsigned sum_blocks = (unsigned)(d.N * segs);
+      const EmptySpans<WT, VZ> empty(gW, ldgw, d);
+      hipLaunchKernelGGL((token_few_kernel<WT, XT, VE, VZ>), dim3(sum_blocks + empty.blocks()),
+                         dim3(256), 0, s, static_cast<const XT*>(g), ldg, of, (int32_t)d.N, d.D,
+                         d.scale, static_cast<WT*>(gW), ldgw, segs, sum_blocks, empty);
+      return hipGetLastError();
+    });
+  }
   hipError_t e;
-  if (L.filtered) {
-    hipLaunchKernelGGL(token_bucket_kernel<true>, dim3(L.buckets), dim3(kBucketThreads),
-                       lds + sizeof(int32_t) * (size_t)d.N, s, of, (int32_t)d.N, nullptr, nullptr, nullptr, off, pos, sid);
-  } else {
-    const SplitShape sh = split_shape(d.N);
+  if (!L.filtered) {
+    const SplitShape sh = split_shape(d.N, L.buckets + 1);
     const int32_t stride = split_stride(L.buckets + 1);
     hipLaunchKernelGGL(token_count_kernel, dim3(sh.tiles), dim3(kSplitThreads), 0, s, of, d.N, sh,
                        stride, at(L.counts));
     if ((e = hipGetLastError()) != hipSuccess) return e;
     hipLaunchKernelGGL(token_split_kernel, dim3(sh.tiles), dim3(kSplitThreads), 0, s, of, d.N, sh,
-                       bits_for(L.buckets + 1), stride, at(L.counts), at(L.bstart), at(L.lpos),
-                       at(L.llow));
+                       bits_for(L.buckets + 1), stride, at(L.counts), at(L.bstart), split);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL(token_bucket_kernel<false>, dim3(L.buckets), dim3(kBucketThreads), lds, s, of,
-                       (int32_t)d.N, at(L.bstart), at(L.lpos), at(L.llow), off, pos, sid);
   }
+  auto sort_buckets = [&](auto threads, auto filter) {
+    constexpr int T = decltype(threads)::value;
+    constexpr bool F = decltype(filter)::value;
+    const size_t lds = sizeof(int32_t) * (((size_t)(T / kWave + 1) << L.shift) + (F ? (size_t)d.N : 0));
+    hipLaunchKernelGGL((token_bucket_kernel<T, F>), dim3(L.buckets), dim3(T), lds, s, of,
+                       (int32_t)d.N, L.chunk, at(L.bstart), split, off, sorted, listed);
+  };
+  using std::bool_constant;
+  using std::integral_constant;
+  if (L.filtered) sort_buckets(integral_constant<int, 512>{}, bool_constant<true>{});
+  else sort_buckets(integral_constant<int, 512>{}, bool_constant<false>{});
   if ((e = hipGetLastError()) != hipSuccess) return e;
+  e = with_gradient_types(d, [&](auto wt, auto xt, auto ve, auto vz) {
+    using WT = decltype(wt);
+    using XT = decltype(xt);
+    constexpr int VE = decltype(ve)::value, VZ = decltype(vz)::value;
+    unsigned sum_blocks = 0;
+    const Units u = make_units(L.chunks, (d.D + kWave * VE - 1) / (kWave * VE), &sum_blocks);
+    const EmptySpans<WT, VZ> empty(gW, ldgw, d);
+    hipLaunchKernelGGL((token_sum_kernel<WT, XT, VE, VZ>), dim3(sum_blocks + empty.blocks()),
+                       dim3(256), 0, s, static_cast<const XT*>(g), ldg, off, sorted, (int32_t)d.V,
+                       d.D, d.scale, static_cast<WT*>(gW), ldgw, runs, parts, L.part_ld, L.chunk,
+                       u, sum_blocks, empty);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess || L.chunks < 2) return e;
   return with_type(d.wdtype, [&](auto wt) {
     using WT = decltype(wt);
-    e = with_type(d.xdtype, [&](auto xt) {
-      using XT = decltype(xt);
-      auto go = [&](auto ve, auto vz) {
-        constexpr int VE = decltype(ve)::value, VZ = decltype(vz)::value;
-        unsigned sum_blocks = 0;
-        const Units u = make_units(L.chunks, (d.D + kWave * VE - 1) / (kWave * VE), &sum_blocks);
-        const unsigned zero_blocks = (unsigned)((d.V + 4 * kZeroRows - 1) / (4 * kZeroRows));
-        hipLaunchKernelGGL((token_sum_kernel<WT, XT, VE, VZ>), dim3(sum_blocks + zero_blocks),
-                           dim3(256), 0, s, static_cast<const XT*>(g), ldg, off, pos, sid,
-                           (int32_t)d.V, d.D, d.scale, static_cast<WT*>(gW), ldgw, parts,
-                           L.part_ld, L.chunk, u, sum_blocks);
-        return hipGetLastError();
-      };
-      using std::integral_constant;
-      if (d.D >= 8)
-        return go(integral_constant<int, pack_elems<XT>()>{}, integral_constant<int, pack_elems<WT>()>{});
-      return go(integral_constant<int, 1>{}, integral_constant<int, 1>{});
-    });
-    if (e != hipSuccess || L.chunks < 2) return e;
-    const unsigned panels = (unsigned)((d.D + 1023) / 1024);
-    hipLaunchKernelGGL(token_join_kernel<WT>,
-                       dim3((unsigned)(L.chunks < (1 << 16) ? L.chunks : (1 << 16)),
-                            panels < 64 ? panels : 64),
-                       dim3(1024), 0, s, off, sid, (int32_t)d.V, d.D, d.scale,
-                       static_cast<WT*>(gW), ldgw, parts, L.part_ld, L.chunk, L.chunks);
+    hipLaunchKernelGGL(token_join_kernel<WT>, dim3(kJoinBlocks), dim3(kJoinWaves * kWave), 0, s,
+                       runs, d.D, d.scale, static_cast<WT*>(gW), ldgw, parts, L.part_ld);
     return hipGetLastError();
   });
 }
