@@ -151,7 +151,7 @@ size_t tbe_distill_workspace_bytes(const tbe_distill_desc* desc);
 
 /* x: device [N, V]. ids, t: device [N, K], dense. loss: device float32 [N],
  * overwritten. stats: device float32 [N, 2], overwritten: the row's largest
- * logit and the sum of exp((x - largest) / tau), for the backward (0 and 1
+ * logit and the sum of exp((x - largest) / tau), for the backward (0 and 0
  * for a row without a teacher). */
 tbe_status tbe_distill_forward(const tbe_distill_desc* desc, const void* x, int64_t ldx,
                                const void* ids, const void* t, float* loss, float* stats,
