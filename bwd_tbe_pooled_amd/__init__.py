@@ -198,7 +198,7 @@ def _stream(stream):
     if stream is None:
         # the handle alone: building torch's Stream object for it costs 2.8 us,
         # as much as a launch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
 
 
@@ -398,6 +398,8 @@ def exported_symbols() -> list:
 
 
 # --- language-model operators (include/tbe_lm.h) ---------------------------------------
+if not os.path.exists(os.path.join(_HERE, "_lmcall.so")):
+    raise ImportError("_lmcall.so is missing: build it with `python bwd_tbe_pooled_amd/build.py`")
 from .lm import (DistillDesc, ExpertDesc, ExpertPlan, TokenDesc,  # noqa: E402,F401
                  distill_workspace, expert_workspace, tbe_distill_backward, tbe_distill_forward,
                  tbe_distill_step, tbe_expert_combine, tbe_expert_combine_backward,

@@ -14,14 +14,12 @@ least its width); ids and per-row vectors are contiguous.
 from __future__ import annotations
 
 import ctypes
-from typing import Optional
 
 import torch
 
-from . import (DTYPE_CODES, TBE_ERR_ARG, TbeError, _TORCH_W, _check, _lib, _stream)
+from . import DTYPE_CODES, TBE_ERR_ARG, TbeError, _check, _lib, _lmcall
 
 _P, _I64, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
-_IDX = {False: torch.int32, True: torch.int64}
 
 
 class tbe_token_desc(ctypes.Structure):
@@ -64,47 +62,10 @@ _distill_backward = _declare("tbe_distill_backward", _P, *_m, _P, _P, _P, _P, *_
 _distill_step = _declare("tbe_distill_step", _P, *_m, _P, _P, _P, _P, *_m, *_ws, _P)
 
 
-def _tensor(t, name, dtype):
-    """Raises for what is not a device tensor of this type."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if not t.is_cuda:
-        raise TypeError(f"{name}: must be a device tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-
-
-def _vec(t, name, dtype, shape):
-    """Device pointer of a contiguous tensor of this shape."""
-    if type(t) is not torch.Tensor or t.dtype is not dtype or not t.is_cuda:
-        _tensor(t, name, dtype)
-    if t.shape != shape:
-        raise TypeError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise TypeError(f"{name}: must be contiguous")
-    return t.data_ptr()
-
-
-def _mat(t, name, dtype, rows, cols, out=False):
-    """Device pointer and row stride of a [rows, cols] matrix."""
-    if type(t) is not torch.Tensor or t.dtype is not dtype or not t.is_cuda:
-        _tensor(t, name, dtype)
-    if t.shape != (rows, cols):
-        raise TypeError(f"{name}: expected shape {(rows, cols)}, got {tuple(t.shape)}")
-    ld, unit = t.stride()
-    if unit != 1 and cols > 1:
-        raise TypeError(f"{name}: columns must be contiguous")
-    if rows <= 1:
-        ld = cols
-    elif out and ld < cols:
-        raise TypeError(f"{name}: rows of an output must not overlap")
-    return t.data_ptr(), ld
-
-
-def _scratch(ws):
-    if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
-        raise TypeError("workspace: expected a contiguous device tensor")
-    return ws.data_ptr(), ws.nbytes
+# checks of a call's tensors, and the call: in C++ (csrc/lm_call.cpp)
+_lmcall.bind(tuple(ctypes.cast(f, _P).value for f in (
+    _token_forward, _token_backward, _expert_plan, _expert_dispatch, _expert_dispatch_backward,
+    _expert_combine, _expert_combine_backward, _distill_forward, _distill_backward, _distill_step)))
 
 
 def _workspace(bytes_of, desc, where, device):
@@ -117,10 +78,9 @@ def _workspace(bytes_of, desc, where, device):
 class _LmDesc:
     """Owns the C description `c`; `ref` is its address."""
 
-    def _own(self, c, idx64):
+    def _own(self, c):
         self.c = c
         self.ref = ctypes.addressof(c)
-        self.idx = _IDX[bool(idx64)]
 
 
 # --- token table -------------------------------------------------------------------
@@ -131,9 +91,8 @@ class TokenDesc(_LmDesc):
     def __init__(self, N: int, V: int, D: int, wdtype: str = "bf16", xdtype: str = "bf16",
                  idx64: bool = True, scale: float = 1.0):
         self.N, self.V, self.D = int(N), int(V), int(D)
-        self.w, self.x = _TORCH_W[wdtype], _TORCH_W[xdtype]
         self._own(tbe_token_desc(self.N, self.V, self.D, DTYPE_CODES[wdtype], DTYPE_CODES[xdtype],
-                                 int(bool(idx64)), float(scale)), idx64)
+                                 int(bool(idx64)), float(scale)))
 
 
 def token_workspace(desc: TokenDesc, device="cuda"):
@@ -143,20 +102,12 @@ def token_workspace(desc: TokenDesc, device="cuda"):
 
 def tbe_token_forward(desc: TokenDesc, W, ids, out, stream=None):
     """out[n] = scale * W[ids[n]]; zeros where the id is outside [0, V)."""
-    N, D = desc.N, desc.D
-    _check(_token_forward(desc.ref, *_mat(W, "W", desc.w, desc.V, D),
-                          _vec(ids, "ids", desc.idx, (N,)),
-                          *_mat(out, "out", desc.x, N, D, True), _stream(stream)),
-           "tbe_token_forward")
+    _check(_lmcall.token_forward(desc.ref, W, ids, out, stream), "tbe_token_forward")
 
 
 def tbe_token_backward(desc: TokenDesc, g, ids, gW, ws, stream=None):
     """gW[v] = scale * sum of g[n] over the tokens with ids[n] = v, all V rows."""
-    N, D = desc.N, desc.D
-    _check(_token_backward(desc.ref, *_mat(g, "g", desc.x, N, D),
-                           _vec(ids, "ids", desc.idx, (N,)),
-                           *_mat(gW, "gW", desc.w, desc.V, D, True), *_scratch(ws),
-                           _stream(stream)), "tbe_token_backward")
+    _check(_lmcall.token_backward(desc.ref, g, ids, gW, ws, stream), "tbe_token_backward")
 
 
 # --- experts -----------------------------------------------------------------------
@@ -166,9 +117,8 @@ class ExpertDesc(_LmDesc):
     def __init__(self, N: int, K: int, E: int, D: int, dtype: str = "bf16", idx64: bool = True):
         self.N, self.K, self.E, self.D = int(N), int(K), int(E), int(D)
         self.M = self.N * self.K
-        self.x = _TORCH_W[dtype]
         self._own(tbe_expert_desc(self.N, self.K, self.E, self.D, DTYPE_CODES[dtype],
-                                  int(bool(idx64))), idx64)
+                                  int(bool(idx64))))
 
 
 class ExpertPlan:
@@ -187,50 +137,28 @@ def expert_workspace(desc: ExpertDesc, device="cuda"):
 
 def tbe_expert_plan(desc: ExpertDesc, ids, plan: ExpertPlan, ws, stream=None):
     """Sorts the assignments by expert into `plan` (dropped ones at the end)."""
-    i32, M = torch.int32, desc.M
-    _check(_expert_plan(desc.ref, _vec(ids, "ids", desc.idx, (desc.N, desc.K)),
-                        _vec(plan.offsets, "plan.offsets", i32, (desc.E + 1,)),
-                        _vec(plan.order, "plan.order", i32, (M,)),
-                        _vec(plan.slots, "plan.slots", i32, (M,)), *_scratch(ws),
-                        _stream(stream)), "tbe_expert_plan")
+    _check(_lmcall.expert_plan(desc.ref, ids, plan.offsets, plan.order, plan.slots, ws, stream), "tbe_expert_plan")
 
 
 def tbe_expert_dispatch(desc: ExpertDesc, x, slots, xs, stream=None):
     """xs[place of (n, k)] = x[n]; zeros at the places of dropped assignments."""
-    _check(_expert_dispatch(desc.ref, *_mat(x, "x", desc.x, desc.N, desc.D),
-                            _vec(slots, "slots", torch.int32, (desc.M,)),
-                            *_mat(xs, "xs", desc.x, desc.M, desc.D, True), _stream(stream)),
-           "tbe_expert_dispatch")
+    _check(_lmcall.expert_dispatch(desc.ref, x, slots, xs, stream), "tbe_expert_dispatch")
 
 
 def tbe_expert_dispatch_backward(desc: ExpertDesc, dxs, slots, dx, stream=None):
     """dx[n] = sum over kept k of dxs[place of (n, k)]."""
-    _check(_expert_dispatch_backward(desc.ref, *_mat(dxs, "dxs", desc.x, desc.M, desc.D),
-                                     _vec(slots, "slots", torch.int32, (desc.M,)),
-                                     *_mat(dx, "dx", desc.x, desc.N, desc.D, True),
-                                     _stream(stream)), "tbe_expert_dispatch_backward")
+    _check(_lmcall.expert_dispatch_backward(desc.ref, dxs, slots, dx, stream), "tbe_expert_dispatch_backward")
 
 
 def tbe_expert_combine(desc: ExpertDesc, ys, slots, w, out, stream=None):
     """out[n] = sum over kept k of w[n, k] * ys[place of (n, k)]."""
-    _check(_expert_combine(desc.ref, *_mat(ys, "ys", desc.x, desc.M, desc.D),
-                           _vec(slots, "slots", torch.int32, (desc.M,)),
-                           _vec(w, "w", torch.float32, (desc.N, desc.K)),
-                           *_mat(out, "out", desc.x, desc.N, desc.D, True), _stream(stream)),
-           "tbe_expert_combine")
+    _check(_lmcall.expert_combine(desc.ref, ys, slots, w, out, stream), "tbe_expert_combine")
 
 
 def tbe_expert_combine_backward(desc: ExpertDesc, dout, ys, slots, w, dys, dw, stream=None):
     """dys[place of (n, k)] = w[n, k] * dout[n], dw[n, k] = <dout[n], ys[place]>;
     zeros where the assignment is dropped. dys may be ys."""
-    N, K, D, M = desc.N, desc.K, desc.D, desc.M
-    _check(_expert_combine_backward(desc.ref, *_mat(dout, "dout", desc.x, N, D),
-                                    *_mat(ys, "ys", desc.x, M, D),
-                                    _vec(slots, "slots", torch.int32, (M,)),
-                                    _vec(w, "w", torch.float32, (N, K)),
-                                    *_mat(dys, "dys", desc.x, M, D, True),
-                                    _vec(dw, "dw", torch.float32, (N, K)), _stream(stream)),
-           "tbe_expert_combine_backward")
+    _check(_lmcall.expert_combine_backward(desc.ref, dout, ys, slots, w, dys, dw, stream), "tbe_expert_combine_backward")
 
 
 # --- distillation --------------------------------------------------------------------
@@ -240,9 +168,8 @@ class DistillDesc(_LmDesc):
     def __init__(self, N: int, V: int, K: int, dtype: str = "bf16", tdtype: str = "f32",
                  idx64: bool = True, temperature: float = 1.0):
         self.N, self.V, self.K = int(N), int(V), int(K)
-        self.x, self.t = _TORCH_W[dtype], _TORCH_W[tdtype]
         self._own(tbe_distill_desc(self.N, self.V, self.K, DTYPE_CODES[dtype], DTYPE_CODES[tdtype],
-                                   int(bool(idx64)), float(temperature)), idx64)
+                                   int(bool(idx64)), float(temperature)))
 
 
 def distill_workspace(desc: DistillDesc, device="cuda"):
@@ -252,31 +179,14 @@ def distill_workspace(desc: DistillDesc, device="cuda"):
 
 def tbe_distill_forward(desc: DistillDesc, x, ids, t, loss, stats, ws, stream=None):
     """loss[n] = tau^2 KL(teacher || student) of row n; stats [N, 2] for the backward."""
-    N, K = desc.N, desc.K
-    _check(_distill_forward(desc.ref, *_mat(x, "x", desc.x, N, desc.V),
-                            _vec(ids, "ids", desc.idx, (N, K)), _vec(t, "t", desc.t, (N, K)),
-                            _vec(loss, "loss", torch.float32, (N,)),
-                            _vec(stats, "stats", torch.float32, (N, 2)), *_scratch(ws),
-                            _stream(stream)), "tbe_distill_forward")
+    _check(_lmcall.distill_forward(desc.ref, x, ids, t, loss, stats, ws, stream), "tbe_distill_forward")
 
 
 def tbe_distill_backward(desc: DistillDesc, x, ids, t, stats, gl, gx, stream=None):
     """gx = gl * tau * (softmax(x / tau) - teacher). gx may be x."""
-    N, K, V = desc.N, desc.K, desc.V
-    _check(_distill_backward(desc.ref, *_mat(x, "x", desc.x, N, V),
-                             _vec(ids, "ids", desc.idx, (N, K)), _vec(t, "t", desc.t, (N, K)),
-                             _vec(stats, "stats", torch.float32, (N, 2)),
-                             _vec(gl, "gl", torch.float32, (N,)),
-                             *_mat(gx, "gx", desc.x, N, V, True), _stream(stream)),
-           "tbe_distill_backward")
+    _check(_lmcall.distill_backward(desc.ref, x, ids, t, stats, gl, gx, stream), "tbe_distill_backward")
 
 
 def tbe_distill_step(desc: DistillDesc, x, ids, t, gl, loss, gx, ws, stream=None):
     """Loss and gradient in one call. gx may be x."""
-    N, K, V = desc.N, desc.K, desc.V
-    _check(_distill_step(desc.ref, *_mat(x, "x", desc.x, N, V),
-                         _vec(ids, "ids", desc.idx, (N, K)), _vec(t, "t", desc.t, (N, K)),
-                         _vec(gl, "gl", torch.float32, (N,)),
-                         _vec(loss, "loss", torch.float32, (N,)),
-                         *_mat(gx, "gx", desc.x, N, V, True), *_scratch(ws), _stream(stream)),
-           "tbe_distill_step")
+    _check(_lmcall.distill_step(desc.ref, x, ids, t, gl, loss, gx, ws, stream), "tbe_distill_step")
