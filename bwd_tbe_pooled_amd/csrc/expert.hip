@@ -241,9 +241,10 @@ SplitShape split_shape(int64_t n, int32_t bins) {
   // one workgroup alone sorts up to 8 rounds a wave faster than two launches
   if (n <= 8192) return SplitShape{1, n > 0 ? (int32_t)((n + 1023) / 1024 * 1024) : 1024};
   // every tile reads all tiles' counts (about 80 bytes a ns) and places 1024
-  // keys a round (about 0.7 us): the sum is least at this number of tiles
+  // keys a round (about 1.4 us): the sum is least at this number of tiles.
+  // 262144 keys in 1001 bins: 12.4 us with 86 tiles, 13.0 with 43, 19.4 with 256.
   int64_t tiles = 1;
-  while (tiles < 256 && tiles * tiles * bins < n * 7) ++tiles;
+  while (tiles < 256 && tiles * tiles * bins < n * 28) ++tiles;
   const int64_t len = ((n + tiles - 1) / tiles + 1023) / 1024 * 1024;
   return SplitShape{(int32_t)((n + len - 1) / len), (int32_t)len};
 }

@@ -9,6 +9,7 @@ using namespace tbe;
 namespace {
 
 constexpr int64_t kI32Lim = (int64_t(1) << 31) - 1;
+constexpr int32_t kMaxD = 1 << 28;  // columns: offsets inside a row stay in 32 bits
 
 #define TBE_TRY_HIP(expr)                                        \
   do {                                                           \
@@ -25,14 +26,14 @@ bool out_ld(int64_t ld, int64_t width) { return ld >= width; }
 tbe_status check(const tbe_token_desc* d) {
   if (!d || d->N < 0 || d->V < 1 || d->D < 1 || !idx_ok(d->idx64)) return TBE_ERR_ARG;
   if (!type_ok(d->wdtype) || !type_ok(d->xdtype)) return TBE_ERR_UNSUPPORTED;
-  if (d->N >= (int64_t(1) << 30) || d->V > kTokenMaxRows) return TBE_ERR_UNSUPPORTED;
+  if (d->N >= (int64_t(1) << 30) || d->V > kTokenMaxRows || d->D > kMaxD) return TBE_ERR_UNSUPPORTED;
   return TBE_OK;
 }
 
 tbe_status check(const tbe_expert_desc* d) {
   if (!d || d->N < 0 || d->K < 1 || d->E < 1 || d->D < 1 || !idx_ok(d->idx64)) return TBE_ERR_ARG;
   if (!type_ok(d->dtype)) return TBE_ERR_UNSUPPORTED;
-  if (d->K > 64 || d->E > kSplitBins - 1 || d->N >= kI32Lim || d->N * d->K >= kI32Lim)
+  if (d->K > 64 || d->E > kSplitBins - 1 || d->D > kMaxD || d->N >= kI32Lim || d->N * d->K >= kI32Lim)
     return TBE_ERR_UNSUPPORTED;
   return TBE_OK;
 }

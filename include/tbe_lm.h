@@ -42,8 +42,8 @@ extern "C" {
  *   backward   gW[v, :]  = scale * sum over n with ids[n] = v of g[n, :]
  * An id outside [0, V) is padding: its output row is zero and it adds nothing
  * to gW. The backward writes all V rows of gW (zeros where no token has the
- * id). 1 <= V <= 1047552 (1023 * 1024), N < 2^30, D >= 1 (else TBE_ERR_ARG or
- * TBE_ERR_UNSUPPORTED). */
+ * id). 1 <= V <= 1047552 (1023 * 1024), N < 2^30, 1 <= D <= 2^28 (else
+ * TBE_ERR_ARG or TBE_ERR_UNSUPPORTED). */
 typedef struct {
     int64_t N;            /* tokens, >= 0 */
     int64_t V;            /* rows of the table */
@@ -76,7 +76,7 @@ tbe_status tbe_token_backward(const tbe_token_desc* desc, const void* g, int64_t
  *   slots[j]    the place of assignment j; ~place (negative) when dropped
  * The other calls read only `slots`. They take a slot outside [-M, M) for a
  * dropped assignment without a place: it is neither read nor written.
- * 1 <= E <= 1023, 1 <= K <= 64, D >= 1, N*K < 2^31 - 1. */
+ * 1 <= E <= 1023, 1 <= K <= 64, 1 <= D <= 2^28, N*K < 2^31 - 1. */
 typedef struct {
     int64_t N;            /* tokens, >= 0 */
     int32_t K;            /* assignments per token */
