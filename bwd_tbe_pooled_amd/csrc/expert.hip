@@ -242,8 +242,9 @@ hipError_t with_width(int32_t D, F f) {
 }  // namespace
 
 SplitShape split_shape(int64_t n, int32_t bins) {
-  // one workgroup alone sorts up to 8 rounds a wave faster than two launches
-  if (n <= 8192) return SplitShape{1, n > 0 ? (int32_t)((n + 1023) / 1024 * 1024) : 1024};
+  // one workgroup alone: 4096 keys in 6.1 us (64 bins; 512 bins 7.2), where two
+  // launches take 7.4 (8.9); 8192 keys in 9.1 (10.7)
+  if (n <= 4096) return SplitShape{1, n > 0 ? (int32_t)((n + 1023) / 1024 * 1024) : 1024};
   // every tile reads all tiles' counts (about 80 bytes a ns) and places 1024
   // keys a round (about 1.4 us): the sum is least at this number of tiles.
   // 262144 keys in 1001 bins: 12.4 us with 86 tiles, 13.0 with 43, 19.4 with 256.

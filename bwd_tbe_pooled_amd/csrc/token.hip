@@ -93,7 +93,10 @@ __global__ __launch_bounds__(kSplitThreads) void token_split_kernel(
     for (int i = threadIdx.x; i <= of.buckets; i += kSplitThreads) bstart[i] = s.start[i];
 }
 
-constexpr int kFilterTokens = 4096;      // tokens a workgroup filters by itself
+// Tokens a workgroup filters by itself: 4096 in 24 us (D 512) against 30 with the
+// split's launches; 8192 would take as long as those.
+constexpr int kFilterTokens = 4096;
+constexpr int kFilterRounds = kFilterTokens / 512;
 constexpr int kRounds = 8;               // rounds of 64 places a wave has in flight
 
 // Sorts one bucket by the lower part of the id: (token, id) at the sorted
@@ -114,7 +117,7 @@ __global__ __launch_bounds__(THREADS) void token_bucket_kernel(
   const int shift = of.shift;
   const int32_t width = 1 << shift;
   uint32_t* const is_long = reinterpret_cast<uint32_t*>(lds + (kWaves << shift));  // [low]
-  int32_t* const list = lds + ((kWaves + 1) << shift);  // FILTER: pos | low << 12
+  int32_t* const list = lds + ((kWaves + 1) << shift);  // FILTER: token | low << 12
   __shared__ int32_t sums[2 * kWaves];
   const int tid = threadIdx.x;
   const int wave = wave_index();
@@ -126,19 +129,19 @@ __global__ __launch_bounds__(THREADS) void token_bucket_kernel(
 
   if constexpr (FILTER) {
     // the wave's span of tokens: those of this bucket and of lower ones
-    static_assert(kFilterTokens <= kRounds * THREADS || !FILTER, "a span is kRounds rounds");
+    static_assert(THREADS == 512 || !FILTER, "a span is kFilterRounds rounds");
     const int32_t span = ((N + THREADS - 1) / THREADS) * kWave;
     const int32_t wa = wave * span;
     const int32_t we = wa + span < N ? wa + span : N;
-    int32_t id[kRounds];
+    int32_t id[kFilterRounds];
 #pragma unroll
-    for (int q = 0; q < kRounds; ++q) {
+    for (int q = 0; q < kFilterRounds; ++q) {
       const int32_t j = wa + q * kWave + lane;
       id[q] = j < we ? of.load(j) : of.none();
     }
     int32_t mine = 0, lower = 0;
 #pragma unroll
-    for (int q = 0; q < kRounds; ++q) {
+    for (int q = 0; q < kFilterRounds; ++q) {
       const int32_t bin = of.bin(id[q]);
       mine += __popcll(__ballot(bin == b));
       lower += __popcll(__ballot(bin < b));
@@ -157,7 +160,7 @@ __global__ __launch_bounds__(THREADS) void token_bucket_kernel(
     }
     if (mine) {
 #pragma unroll
-      for (int q = 0; q < kRounds; ++q) {
+      for (int q = 0; q < kFilterRounds; ++q) {
         const bool ok = of.bin(id[q]) == b;
         const uint64_t m = __ballot(ok);
         if (ok)
@@ -506,14 +509,16 @@ __global__ __launch_bounds__(kJoinWaves * kWave) void token_join_kernel(
 // segment of columns; the first token of an id sums the rows of all tokens of
 // that id, a quarter of them per wave, the others leave. One of the second
 // kind writes zeros over 1024 vectors of the table, but for rows that have a
-// token. Each finds its tokens by looking at all ids, 4 a thread at most: that
-// is cheaper than the launches of the sort, 30 us against 40 for 777 tokens and
-// a table of 132 MB. Every workgroup of a token looks at all ids, so their
-// number is limited; beyond it, and beyond 1024 tokens, the sort is used.
-constexpr int kFewTokens = 1024;
-constexpr int kFewIds = kFewTokens / 256;  // ids per thread
+// token. Each finds its tokens by looking at all ids: that is cheaper than the
+// launches of the sort, 30 us against 40 for 777 tokens and a table of 132 MB, 6
+// against 20 for 1024 tokens and 8 MB. A workgroup costs about 0.7 + 0.9 N / 1024
+// ns of the whole card, the sort's launches about 17 us: both are equal where
+// N (tokens) segments (768 + N) is 18 M. And a frequent id's rows are summed by
+// one workgroup, at 32 rows a us, which 2048 tokens bound.
+constexpr int kFewTokens = 2048;
 
-template <typename WT, typename XT, int VE, int VZ>
+// IDS: ids per thread
+template <typename WT, typename XT, int VE, int VZ, int IDS>
 __global__ __launch_bounds__(256) void token_few_kernel(
     const XT* __restrict__ g, int64_t ldg, BucketOf of, int32_t N, int32_t D, float scale,
     WT* __restrict__ gW, int64_t ldgw, int32_t segs, uint32_t sum_blocks,
@@ -523,15 +528,15 @@ __global__ __launch_bounds__(256) void token_few_kernel(
   __shared__ union {
     struct {
       float part[3][kWave][VE];
-      int32_t token[kFewTokens];
-      int32_t count[kFewIds * 4];
+      int32_t token[IDS * 256];
+      int32_t count[IDS * 4];
     } s;
     uint32_t used[kUsedWords];
   } l;
   const int tid = threadIdx.x, lane = lane_id(), wave = wave_index();
-  int32_t id[kFewIds];  // of token q * 256 + tid
+  int32_t id[IDS];  // of token q * 256 + tid
 #pragma unroll
-  for (int q = 0; q < kFewIds; ++q) id[q] = q * 256 + tid < N ? of.load(q * 256 + tid) : of.none();
+  for (int q = 0; q < IDS; ++q) id[q] = q * 256 + tid < N ? of.load(q * 256 + tid) : of.none();
 
   if (blockIdx.x >= sum_blocks) {
     uint32_t rem;
@@ -539,7 +544,7 @@ __global__ __launch_bounds__(256) void token_few_kernel(
     if (tid < kUsedWords) l.used[tid] = 0;
     __syncthreads();
 #pragma unroll
-    for (int q = 0; q < kFewIds; ++q) {
+    for (int q = 0; q < IDS; ++q) {
       const int64_t r = id[q] - row0;
       if (id[q] >= 0 && r >= 0 && r < 32 * kUsedWords) atomicOr(&l.used[r / 32], 1u << (r % 32));
     }
@@ -552,22 +557,22 @@ __global__ __launch_bounds__(256) void token_few_kernel(
   const int32_t v = of.load(n);
   if (v < 0) return;
   bool earlier = false;
-  uint64_t mine[kFewIds];
+  uint64_t mine[IDS];
 #pragma unroll
-  for (int q = 0; q < kFewIds; ++q) {
+  for (int q = 0; q < IDS; ++q) {
     earlier |= id[q] == v && q * 256 + tid < n;
     mine[q] = __ballot(id[q] == v);
     if (lane == 0) l.s.count[q * 4 + wave] = __popcll(mine[q]);
   }
   if (__syncthreads_or(earlier)) return;
-  int32_t m = 0, at[kFewIds];
+  int32_t m = 0, at[IDS];
 #pragma unroll
-  for (int i = 0; i < kFewIds * 4; ++i) {
+  for (int i = 0; i < IDS * 4; ++i) {
     if (i % 4 == wave) at[i / 4] = m;
     m += l.s.count[i];
   }
 #pragma unroll
-  for (int q = 0; q < kFewIds; ++q)
+  for (int q = 0; q < IDS; ++q)
     if (id[q] == v) l.s.token[at[q] + __popcll(mine[q] & lanes_below())] = q * 256 + tid;
   __syncthreads();
 
@@ -650,7 +655,7 @@ TokenLayout token_layout(const tbe_token_desc& d) {
   // 32 sorted places a wave, 16 where that leaves the chip without waves
   const int32_t vec = d.xdtype == TBE_F32 ? 4 : 8;
   const int64_t segs = (d.D + 64 * vec - 1) / (64 * vec);
-  L.few = d.N <= kFewTokens && d.N * segs <= 8 * kFewTokens;
+  L.few = d.N <= kFewTokens && d.N * segs * (768 + d.N) <= (18 << 20);
   L.chunk = d.N * segs >= kMaxChunk * 2048 ? kMaxChunk : 16;
   L.chunks = (d.N + L.chunk - 1) / L.chunk;
   L.part_ld = ((int64_t)d.D + 3) / 4 * 4;
@@ -712,10 +717,16 @@ hipError_t launch_token_backward(const tbe_token_desc& d, const TokenLayout& L, 
       const int32_t segs = (d.D + kWave * VE - 1) / (kWave * VE);
       const unsigned sum_blocks = (unsigned)(d.N * segs);
       const EmptySpans<WT, VZ> empty(gW, ldgw, d);
-      hipLaunchKernelGGL((token_few_kernel<WT, XT, VE, VZ>), dim3(sum_blocks + empty.blocks()),
-                         dim3(256), 0, s, static_cast<const XT*>(g), ldg, of, (int32_t)d.N, d.D,
-                         d.scale, static_cast<WT*>(gW), ldgw, segs, sum_blocks, empty);
-      return hipGetLastError();
+      auto go = [&](auto ids_per_thread) {
+        hipLaunchKernelGGL((token_few_kernel<WT, XT, VE, VZ, decltype(ids_per_thread)::value>),
+                           dim3(sum_blocks + empty.blocks()), dim3(256), 0, s,
+                           static_cast<const XT*>(g), ldg, of, (int32_t)d.N, d.D, d.scale,
+                           static_cast<WT*>(gW), ldgw, segs, sum_blocks, empty);
+        return hipGetLastError();
+      };
+      if (d.N <= 512) return go(std::integral_constant<int, 2>{});
+      if (d.N <= 1024) return go(std::integral_constant<int, 4>{});
+      return go(std::integral_constant<int, kFewTokens / 256>{});
     });
   }
   hipError_t e;

@@ -130,14 +130,14 @@ def test_distill_rows_without_a_teacher_are_marked_by_their_statistics():
 
 
 # --- token table -----------------------------------------------------------------------
-# few tokens without a sort (up to 1024, fewer of wide rows), one launch's sort
+# few tokens without a sort (up to 2048, fewer of wide rows), one launch's sort
 # (up to 4096), three beyond; tables whose rows and spans of 1024 vectors end apart
-TOKEN = [(N, V, D, w, x, dist) for N in (1, 2, 1023, 1024, 1025) for (V, D, w, x) in
+TOKEN = [(N, V, D, w, x, dist) for N in (1, 2, 512, 513, 1023, 1024, 1025, 2048, 2049) for (V, D, w, x) in
          [(97, 1030, "f32", "f16"), (5000, 8, "bf16", "bf16"), (1, 700, "f16", "f32")]
          for dist in ("same", "square")] + [
     (1024, 50, 4100, "bf16", "f32", "few"),     # 17 segments: over the few tokens' limit
-    (481, 50, 4100, "bf16", "f32", "square"),   # just under
-    (482, 50, 4100, "bf16", "f32", "square"),
+    (736, 50, 4100, "bf16", "f32", "square"),   # just under
+    (737, 50, 4100, "bf16", "f32", "square"),
     (4096, 1023 * 1024, 9, "bf16", "bf16", "square"),
     (4097, 1023 * 1024, 9, "f16", "f32", "square"),
     (4096, 700, 260, "f32", "f32", "same"),
