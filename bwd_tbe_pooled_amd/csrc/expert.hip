@@ -58,6 +58,25 @@ struct Slot {
   }
 };
 
+// The token's K slots (and weights), one per lane, from one load: as scalars
+// each would be waited for before its row.
+struct TokenSlots {
+  int32_t slot;
+  float w;
+  __device__ __forceinline__ TokenSlots(const int32_t* __restrict__ slots,
+                                        const float* __restrict__ weights, int64_t n, int32_t K) {
+    const int lane = lane_id();
+    slot = lane < K ? slots[n * K + lane] : INT32_MIN;
+    w = lane < K && weights ? weights[n * K + lane] : 1.f;
+  }
+  __device__ __forceinline__ Slot at(int32_t k, int32_t M) const {
+    return Slot(__builtin_amdgcn_readlane(slot, k), M);
+  }
+  __device__ __forceinline__ float weight(int32_t k) const {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), k));
+  }
+};
+
 template <typename T, int VE, int U>
 __global__ __launch_bounds__(256) void expert_dispatch_kernel(
     const T* __restrict__ x, int64_t ldx, const int32_t* __restrict__ slots, int32_t K, int32_t M,
@@ -67,13 +86,13 @@ __global__ __launch_bounds__(256) void expert_dispatch_kernel(
   for (UnitWalk u(units, blockIdx.x * 4 + wave_index()); u.valid(units); u.next(units)) {
     const T* row = x + u.row * ldx;
     const int32_t i0 = u.seg * (U * kWave) + lane_id();
+    const TokenSlots sl(slots, nullptr, u.row, K);
     R v[U];
 #pragma unroll
     for (int i = 0; i < U; ++i)
       if (i0 + i * kWave < nv) v[i] = load_pack_once<T, VE>(row + pack_column<VE>(i0 + i * kWave, D));
-    const int32_t* sl = slots + u.row * K;
     for (int32_t k = 0; k < K; ++k) {
-      const Slot s(sl[k], M);
+      const Slot s = sl.at(k, M);
       if (!s.has) continue;
       T* to = xs + (int64_t)s.place * ldxs;
       R zero;
@@ -101,16 +120,17 @@ __global__ __launch_bounds__(256) void expert_combine_kernel(
     for (int i = 0; i < U; ++i)
 #pragma unroll
       for (int e = 0; e < VE; ++e) acc[i][e] = 0.f;
-    const int32_t* sl = slots + u.row * K;
+    const TokenSlots sl(slots, w, u.row, K);
     constexpr int KU = 4;  // rows in flight
     for (int32_t k0 = 0; k0 < K; k0 += KU) {
       R v[KU][U];
       float wk[KU];
 #pragma unroll
       for (int q = 0; q < KU; ++q) {
-        const Slot s(k0 + q < K ? sl[k0 + q] : -1, M);
+        const int32_t k = k0 + q < K ? k0 + q : K - 1;
+        const Slot s = sl.at(k, M);
         const bool use = k0 + q < K && s.kept;
-        wk[q] = use ? (w ? w[u.row * K + k0 + q] : 1.f) : 0.f;
+        wk[q] = use ? sl.weight(k) : 0.f;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
           zero_raw(v[q][i]);
@@ -161,7 +181,7 @@ __global__ __launch_bounds__(256) void expert_combine_backward_kernel(
     if (lane < K) dots[wave][lane] = 0.f;
     wave_lds_sync();
     if (live) {
-      const int32_t* sl = slots + n * K;
+      const TokenSlots sl(slots, w, n, K);
       for (int32_t p0 = part * kWave + lane; p0 - lane < nv; p0 += U * WPT * kWave) {
         float d[U][VE];
         int32_t col[U], skip[U];
@@ -184,7 +204,7 @@ __global__ __launch_bounds__(256) void expert_combine_backward_kernel(
           bool kept[KU], has[KU];
 #pragma unroll
           for (int q = 0; q < KU; ++q) {
-            const Slot s(k0 + q < K ? sl[k0 + q] : -1, M);
+            const Slot s = sl.at(k0 + q < K ? k0 + q : K - 1, M);
             place[q] = s.place;
             kept[q] = k0 + q < K && s.kept;
             has[q] = k0 + q < K && s.has;
@@ -198,7 +218,7 @@ __global__ __launch_bounds__(256) void expert_combine_backward_kernel(
 #pragma unroll
           for (int q = 0; q < KU; ++q) {
             if (!has[q]) continue;
-            const float wk = kept[q] ? w[n * K + k0 + q] : 0.f;
+            const float wk = kept[q] ? sl.weight(k0 + q) : 0.f;
             float dot = 0.f;
 #pragma unroll
             for (int i = 0; i < U; ++i) {

@@ -136,8 +136,8 @@ TOKEN = [(N, V, D, w, x, dist) for N in (1, 2, 512, 513, 1023, 1024, 1025, 2048,
          [(97, 1030, "f32", "f16"), (5000, 8, "bf16", "bf16"), (1, 700, "f16", "f32")]
          for dist in ("same", "square")] + [
     (1024, 50, 4100, "bf16", "f32", "few"),     # 17 segments: over the few tokens' limit
-    (736, 50, 4100, "bf16", "f32", "square"),   # just under
-    (737, 50, 4100, "bf16", "f32", "square"),
+    (737, 50, 4100, "bf16", "f32", "square"),   # just under
+    (738, 50, 4100, "bf16", "f32", "square"),
     (4096, 1023 * 1024, 9, "bf16", "bf16", "square"),
     (4097, 1023 * 1024, 9, "f16", "f32", "square"),
     (4096, 700, 260, "f32", "f32", "same"),
