@@ -129,6 +129,46 @@ def test_distill_rows_without_a_teacher_are_marked_by_their_statistics():
     assert torch.equal(stats[rest][some][:, 0], xs[rest].amax(1)[some])
 
 
+@pytest.mark.parametrize("x", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("V", [65, 515, 1027, 9001, 70003])
+@pytest.mark.parametrize("first", [0, 1, 2, 3, 7])
+def test_distill_alignments(x, V, first):
+    """Logits and gradient that start at different elements of 16 bytes, rows of
+    an odd and of an aligned length; the elements around them stay. The first and
+    last places have a teacher's entry."""
+    say("distill alignments", x, V, first)
+    tbe = lib()
+    for N in (9, 300 if V < 9001 else 20):
+        xs, ids, ts, gl = distill_case(gen(V + first), N, V, 6, x, "f32", True, 0.2)
+        ids[0, :4] = torch.tensor([0, V - 1, 7, V - 8])
+        want_l, want_g, bl, bg = distill_ref(xs, ids, ts, 1.0, gl)
+        desc = tbe.DistillDesc(N, V, 6, dtype=x)
+        for pad in (1, 16):
+            wide = torch.full((N, V + 7 + pad), float("nan"), dtype=DT[x], device="cuda")
+            inp = wide[:, first:first + V]
+            inp.copy_(xs)
+            out = torch.full((N, V + 8), float("nan"), dtype=DT[x], device="cuda")
+            grad = out[:, 3:3 + V]
+            loss, stats = torch.empty(N, device="cuda"), torch.empty(N, 2, device="cuda")
+            ws = tbe.distill_workspace(desc)
+
+            def check():
+                close(loss, want_l, bl, "f32", "loss")
+                close(grad, want_g, bg, x, "gradient")
+                assert torch.isnan(out[:, :3]).all() and torch.isnan(out[:, 3 + V:]).all()
+                out.fill_(float("nan"))
+            tbe.tbe_distill_step(desc, inp, ids, ts, gl, loss, grad, ws)
+            check()
+            tbe.tbe_distill_forward(desc, inp, ids, ts, loss, stats, ws)
+            tbe.tbe_distill_backward(desc, inp, ids, ts, stats, gl, grad)
+            check()
+            tbe.tbe_distill_backward(desc, inp, ids, ts, stats, gl, inp)   # in place
+            close(inp, want_g, bg, x, "gradient in place")
+            rest = torch.ones(V + 7 + pad, dtype=torch.bool, device="cuda")
+            rest[first:first + V] = False
+            assert torch.isnan(wide[:, rest]).all()
+
+
 # --- token table -----------------------------------------------------------------------
 # few tokens without a sort (up to 2048, fewer of wide rows), one launch's sort
 # (up to 4096), three beyond; tables whose rows and spans of 1024 vectors end apart
