@@ -692,7 +692,8 @@ unsigned grid_for(int64_t n) { return (unsigned)(n < (1 << 20) ? n : (1 << 20));
 
 constexpr int64_t kFewRows = 256;             // a row per CU
 // The Infinity Cache: logits of up to its size stay there for the backward if
-// the forward's loads are ordinary ones (1001 x 50021 f16, both: 90 us to 101).
+// the forward's loads are ordinary ones (1001 x 50021 f16: with nontemporal ones
+// both calls together took a tenth longer).
 constexpr int64_t kCacheBytes = 256 << 20;
 
 hipError_t launch_rows(const tbe_distill_desc& d, const void* x, int64_t ldx, const void* ids,
