@@ -17,7 +17,7 @@ import ctypes
 
 import torch
 
-from . import DTYPE_CODES, TBE_ERR_ARG, TbeError, _check, _lib, _lmcall
+from . import DTYPE_CODES, TBE_ERR_ARG, TbeError, _lib, _lmcall
 
 _P, _I64, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
 
@@ -102,12 +102,16 @@ def token_workspace(desc: TokenDesc, device="cuda"):
 
 def tbe_token_forward(desc: TokenDesc, W, ids, out, stream=None):
     """out[n] = scale * W[ids[n]]; zeros where the id is outside [0, V)."""
-    _check(_lmcall.token_forward(desc.ref, W, ids, out, stream), "tbe_token_forward")
+    status = _lmcall.token_forward(desc.ref, W, ids, out, stream)
+    if status:
+        raise TbeError(status, "tbe_token_forward")
 
 
 def tbe_token_backward(desc: TokenDesc, g, ids, gW, ws, stream=None):
     """gW[v] = scale * sum of g[n] over the tokens with ids[n] = v, all V rows."""
-    _check(_lmcall.token_backward(desc.ref, g, ids, gW, ws, stream), "tbe_token_backward")
+    status = _lmcall.token_backward(desc.ref, g, ids, gW, ws, stream)
+    if status:
+        raise TbeError(status, "tbe_token_backward")
 
 
 # --- experts -----------------------------------------------------------------------
@@ -137,28 +141,38 @@ def expert_workspace(desc: ExpertDesc, device="cuda"):
 
 def tbe_expert_plan(desc: ExpertDesc, ids, plan: ExpertPlan, ws, stream=None):
     """Sorts the assignments by expert into `plan` (dropped ones at the end)."""
-    _check(_lmcall.expert_plan(desc.ref, ids, plan.offsets, plan.order, plan.slots, ws, stream), "tbe_expert_plan")
+    status = _lmcall.expert_plan(desc.ref, ids, plan.offsets, plan.order, plan.slots, ws, stream)
+    if status:
+        raise TbeError(status, "tbe_expert_plan")
 
 
 def tbe_expert_dispatch(desc: ExpertDesc, x, slots, xs, stream=None):
     """xs[place of (n, k)] = x[n]; zeros at the places of dropped assignments."""
-    _check(_lmcall.expert_dispatch(desc.ref, x, slots, xs, stream), "tbe_expert_dispatch")
+    status = _lmcall.expert_dispatch(desc.ref, x, slots, xs, stream)
+    if status:
+        raise TbeError(status, "tbe_expert_dispatch")
 
 
 def tbe_expert_dispatch_backward(desc: ExpertDesc, dxs, slots, dx, stream=None):
     """dx[n] = sum over kept k of dxs[place of (n, k)]."""
-    _check(_lmcall.expert_dispatch_backward(desc.ref, dxs, slots, dx, stream), "tbe_expert_dispatch_backward")
+    status = _lmcall.expert_dispatch_backward(desc.ref, dxs, slots, dx, stream)
+    if status:
+        raise TbeError(status, "tbe_expert_dispatch_backward")
 
 
 def tbe_expert_combine(desc: ExpertDesc, ys, slots, w, out, stream=None):
     """out[n] = sum over kept k of w[n, k] * ys[place of (n, k)]."""
-    _check(_lmcall.expert_combine(desc.ref, ys, slots, w, out, stream), "tbe_expert_combine")
+    status = _lmcall.expert_combine(desc.ref, ys, slots, w, out, stream)
+    if status:
+        raise TbeError(status, "tbe_expert_combine")
 
 
 def tbe_expert_combine_backward(desc: ExpertDesc, dout, ys, slots, w, dys, dw, stream=None):
     """dys[place of (n, k)] = w[n, k] * dout[n], dw[n, k] = <dout[n], ys[place]>;
     zeros where the assignment is dropped. dys may be ys."""
-    _check(_lmcall.expert_combine_backward(desc.ref, dout, ys, slots, w, dys, dw, stream), "tbe_expert_combine_backward")
+    status = _lmcall.expert_combine_backward(desc.ref, dout, ys, slots, w, dys, dw, stream)
+    if status:
+        raise TbeError(status, "tbe_expert_combine_backward")
 
 
 # --- distillation --------------------------------------------------------------------
@@ -179,14 +193,20 @@ def distill_workspace(desc: DistillDesc, device="cuda"):
 
 def tbe_distill_forward(desc: DistillDesc, x, ids, t, loss, stats, ws, stream=None):
     """loss[n] = tau^2 KL(teacher || student) of row n; stats [N, 2] for the backward."""
-    _check(_lmcall.distill_forward(desc.ref, x, ids, t, loss, stats, ws, stream), "tbe_distill_forward")
+    status = _lmcall.distill_forward(desc.ref, x, ids, t, loss, stats, ws, stream)
+    if status:
+        raise TbeError(status, "tbe_distill_forward")
 
 
 def tbe_distill_backward(desc: DistillDesc, x, ids, t, stats, gl, gx, stream=None):
     """gx = gl * tau * (softmax(x / tau) - teacher). gx may be x."""
-    _check(_lmcall.distill_backward(desc.ref, x, ids, t, stats, gl, gx, stream), "tbe_distill_backward")
+    status = _lmcall.distill_backward(desc.ref, x, ids, t, stats, gl, gx, stream)
+    if status:
+        raise TbeError(status, "tbe_distill_backward")
 
 
 def tbe_distill_step(desc: DistillDesc, x, ids, t, gl, loss, gx, ws, stream=None):
     """Loss and gradient in one call. gx may be x."""
-    _check(_lmcall.distill_step(desc.ref, x, ids, t, gl, loss, gx, ws, stream), "tbe_distill_step")
+    status = _lmcall.distill_step(desc.ref, x, ids, t, gl, loss, gx, ws, stream)
+    if status:
+        raise TbeError(status, "tbe_distill_step")
