@@ -160,10 +160,15 @@ __global__ __launch_bounds__(256) void expert_combine_kernel(
 // dys[place] = w * dout[n], dw[n,k] = <dout[n], ys[place]>. WPT waves share a
 // token; each keeps up to U vectors per lane of dout in registers over the K
 // places, and wider rows go panel by panel with the partial dots in LDS.
-// dys may be ys: a lane reads its vector of ys before it stores there. (A
-// row's last vector overlaps the one before it; the columns it reads twice
-// are left out of the dot.)
-template <typename T, int VE, int U, int WPT>
+// dys may be ys: a lane reads its vector of ys before it stores there. A row's
+// last vector overlaps the one before it, which another wave may have: the
+// columns it reads twice are left out of its dot, and with IN_PLACE it stores
+// the others alone, element by element. So a column is stored only by the lane
+// whose dot takes it, and no order among the lanes matters. (Whole vectors and
+// single elements after them, in place or not, took 164 us in place of 137 at
+// 20000 x 4 rows of 1029 bf16: a load and a store more per place. Asked at run
+// time instead of by IN_PLACE it cost calls of a few hundred tokens 2 to 4%.)
+template <typename T, int VE, int U, int WPT, bool IN_PLACE>
 __global__ __launch_bounds__(256) void expert_combine_backward_kernel(
     const T* __restrict__ dout, int64_t lddo, const T* ys, int64_t ldys,
     const int32_t* __restrict__ slots, const float* __restrict__ w, int64_t N, int32_t K,
@@ -230,8 +235,17 @@ __global__ __launch_bounds__(256) void expert_combine_backward_kernel(
                 dot = e >= skip[i] ? t : dot;
                 o[e] = kept[q] ? wk * d[i][e] : 0.f;
               }
-              if (in[i])
-                store_pack_once<T, VE>(dys + (int64_t)place[q] * lddys + col[i], narrow<T, VE>(o));
+              if (!in[i]) continue;
+              T* to = dys + (int64_t)place[q] * lddys + col[i];
+              const R r = narrow<T, VE>(o);
+              if (IN_PLACE && skip[i] > 0) {
+                const T* own = reinterpret_cast<const T*>(&r);
+#pragma unroll
+                for (int e = 0; e < VE; ++e)
+                  if (e >= skip[i]) to[e] = own[e];
+              } else {
+                store_pack_once<T, VE>(to, r);
+              }
             }
             dot = wave_sum(dot);
             if (kept[q] && lane == 0) dots[wave][k0 + q] += dot;
@@ -343,19 +357,25 @@ hipError_t launch_expert_combine_backward(const tbe_expert_desc& d, const void* 
     return with_width<T>(d.D, [&](auto ve) {
       constexpr int VE = decltype(ve)::value;
       constexpr int U = 2;
-      auto go = [&](auto wpt) {
+      auto go = [&](auto wpt, auto in_place) {
         constexpr int WPT = decltype(wpt)::value;
+        constexpr bool IN_PLACE = decltype(in_place)::value;
         const int64_t need = (d.N * WPT + 3) / 4;
         const unsigned blocks = (unsigned)(need < (1 << 20) ? need : (1 << 20));
-        hipLaunchKernelGGL((expert_combine_backward_kernel<T, VE, U, WPT>), dim3(blocks), dim3(256),
-                           0, s, static_cast<const T*>(dout), lddo, static_cast<const T*>(ys), ldys,
-                           slots, w, d.N, d.K, (int32_t)(d.N * d.K), d.D, static_cast<T*>(dys),
-                           lddys, dw);
+        hipLaunchKernelGGL((expert_combine_backward_kernel<T, VE, U, WPT, IN_PLACE>), dim3(blocks),
+                           dim3(256), 0, s, static_cast<const T*>(dout), lddo,
+                           static_cast<const T*>(ys), ldys, slots, w, d.N, d.K,
+                           (int32_t)(d.N * d.K), d.D, static_cast<T*>(dys), lddys, dw);
         return hipGetLastError();
       };
       // one wave holds U vectors per lane of a row; wider rows take four
-      if ((d.D + VE - 1) / VE <= U * kWave) return go(std::integral_constant<int, 1>{});
-      return go(std::integral_constant<int, 4>{});
+      auto with_waves = [&](auto in_place) {
+        if ((d.D + VE - 1) / VE <= U * kWave) return go(std::integral_constant<int, 1>{}, in_place);
+        return go(std::integral_constant<int, 4>{}, in_place);
+      };
+      if constexpr (VE > 1)
+        if (dys == ys && d.D % VE) return with_waves(std::true_type{});
+      return with_waves(std::false_type{});
     });
   });
 }

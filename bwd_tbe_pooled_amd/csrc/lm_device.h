@@ -157,7 +157,8 @@ constexpr int pack_elems() {
 
 // First column of a lane's vector i (in vectors of VE columns from column 0).
 // The last vector of a row is moved back to end at D, so it is whole and
-// stores columns of its neighbour again, with the same values. Needs D >= VE.
+// stores columns of its neighbour again, with the same values; where the output
+// is also an input it must not. Needs D >= VE.
 template <int VE>
 __device__ __forceinline__ int32_t pack_column(int32_t i, int32_t D) {
   const int64_t c = (int64_t)i * VE;
