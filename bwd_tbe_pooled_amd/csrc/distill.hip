@@ -47,6 +47,12 @@ struct Shift {
   __device__ __forceinline__ float of(float x, float a) const {
     return far ? (x - m) * a : fmaf(x, a, -c);
   }
+  // The power of the maximum: 1 but for c's rounding, by which every power of
+  // the row is off. (The statistics are given without it: they are the sum of
+  // exp((x - max) / tau) for any reader, not for this shift alone.)
+  __device__ __forceinline__ float of_max(float a) const {
+    return far ? 1.f : exp2_of(fmaf(m, a, -c));
+  }
 };
 
 // Factor from the powers' sum with maximum m to that with the maximum of `to`.
@@ -570,7 +576,7 @@ __global__ __launch_bounds__(BS < 256 ? 256 : BS) void distill_row_kernel(
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) sum += red[group][5][w];
       if (loss) loss[n] = g.tau * sum;
-      if (stats) stats[2 * n] = r.m, stats[2 * n + 1] = r.s;
+      if (stats) stats[2 * n] = r.m, stats[2 * n + 1] = r.s / sh.of_max(g.a);
     }
     if (gx) write_places<XT, BS>(g, T, to, gt, 0, g.V, sh, c, cs);
     group_sync<BS>();  // the next row takes the LDS
@@ -658,9 +664,9 @@ __global__ __launch_bounds__(256) void distill_backward_kernel(
       }
       if (lane == 0) places[group] = here;
     }
-    const float c = gl[n] * g.tau;
-    const float cs = c / s;
     const Shift sh(m, g.a, kFarRow);
+    const float c = gl[n] * g.tau;
+    const float cs = c / (s * sh.of_max(g.a));
     if (x == gx) group_sync<BS>();  // the places are read before they are written
     if (__builtin_expect(sh.far, 0)) {
       far_gradient<XT, BS>(row, to, v0, v1, gt, m, g.a, cs);
