@@ -97,6 +97,33 @@ def teacher(N, g):
 
 @pytest.mark.parametrize("tau", [1.0, 0.7])
 @pytest.mark.parametrize("x", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("V", [37, 1003, 3001, 20011, 70001, 140003])
+def test_far_and_masked_rows(x, V, tau):
+    say("distill bounds", x, V, tau)
+    tbe = lib()
+    kinds, xs, places = rows(x, V, tau, V)
+    # each kind once, and often enough for the variants of many rows
+    for times in (1, 24):
+        if times > 1 and V > 3001:
+            continue
+        xr = xs.repeat(times, 1)
+        N = xr.shape[0]
+        g = gen(V + times)
+        ids = places.expand(N, 5).contiguous()
+        ts = teacher(N, g)
+        gl = torch.randn(N, generator=g).cuda()
+        want = Ref(xr, ids, ts, tau, gl)
+        desc = tbe.DistillDesc(N, V, 5, dtype=x, temperature=tau)
+        outs = run_distill(tbe, desc, xr, ids, ts, gl)
+        for loss, grad in (outs[:2], outs[2:]):
+            for i, kind in enumerate(kinds):
+                sl = slice(i, None, len(kinds))
+                close(loss[sl], want.loss[sl], want.bl[sl], "f32", f"loss, {kind}")
+                close(grad[sl], want.gx[sl], want.bg[sl], x, f"gradient, {kind}")
+
+
+@pytest.mark.parametrize("tau", [1.0, 0.7])
+@pytest.mark.parametrize("x", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("V", [37, 1003, 20011, 140003])
 def test_statistics(x, V, tau):
     """Largest logit and sum of exp((x - largest) / tau); the backward takes such
