@@ -47,18 +47,29 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _hip_include() -> str:
+    """The directory HIPCC has HIP's headers from. The compiler is asked, as it may
+    be a name found on PATH or a wrapper outside the ROCm tree."""
+    cmd = [HIPCC, "-x", "hip", "--offload-host-only", "-M", "-"]
+    r = subprocess.run(cmd, input="#include <hip/hip_runtime_api.h>\n", capture_output=True, text=True)
+    tail = os.path.join("hip", "hip_runtime_api.h")
+    for path in r.stdout.split():
+        if r.returncode == 0 and path.endswith(os.sep + tail):
+            return os.path.abspath(path[:-len(tail)])
+    raise RuntimeError(f"HIP's headers not found\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+
+
 def _build_calls() -> None:
     """Host code only: it looks into torch's tensors and calls through addresses."""
     import sysconfig
 
     import torch
     root = os.path.dirname(torch.__file__)
-    rocm = os.path.dirname(os.path.dirname(HIPCC))
     tmp = CALLS + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-I", INCLUDE,
-           "-isystem", os.path.join(root, "include"), "-isystem", os.path.join(rocm, "include"),
+           "-isystem", os.path.join(root, "include"), "-isystem", _hip_include(),
            "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "lm_call.cpp"), "-o", tmp,
            "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"]
     r = subprocess.run(cmd, capture_output=True, text=True)
