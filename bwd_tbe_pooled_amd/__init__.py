@@ -398,10 +398,22 @@ def exported_symbols() -> list:
 
 
 # --- language-model operators (include/tbe_lm.h) ---------------------------------------
-if not os.path.exists(os.path.join(_HERE, "_lmcall.so")):
-    raise ImportError("_lmcall.so is missing: build it with `python bwd_tbe_pooled_amd/build.py`")
-from .lm import (DistillDesc, ExpertDesc, ExpertPlan, TokenDesc,  # noqa: E402,F401
-                 distill_workspace, expert_workspace, tbe_distill_backward, tbe_distill_forward,
-                 tbe_distill_step, tbe_expert_combine, tbe_expert_combine_backward,
-                 tbe_expert_dispatch, tbe_expert_dispatch_backward, tbe_expert_plan,
-                 tbe_token_backward, tbe_token_forward, token_workspace)
+# Loaded at first use: they need _lmcall.so, an extension for one Python and one
+# torch, where the calls above need libtbe.so alone.
+_LM_NAMES = ("DistillDesc", "ExpertDesc", "ExpertPlan", "TokenDesc", "distill_workspace",
+             "expert_workspace", "tbe_distill_backward", "tbe_distill_forward", "tbe_distill_step",
+             "tbe_expert_combine", "tbe_expert_combine_backward", "tbe_expert_dispatch",
+             "tbe_expert_dispatch_backward", "tbe_expert_plan", "tbe_token_backward",
+             "tbe_token_forward", "token_workspace")
+
+
+def __getattr__(name):
+    if name not in _LM_NAMES:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import lm
+    globals().update((n, getattr(lm, n)) for n in _LM_NAMES)
+    return globals()[name]
+
+
+def __dir__():
+    return sorted({*globals(), *_LM_NAMES})

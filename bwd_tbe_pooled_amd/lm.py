@@ -17,7 +17,13 @@ import ctypes
 
 import torch
 
-from . import DTYPE_CODES, TBE_ERR_ARG, TbeError, _lib, _lmcall
+from . import DTYPE_CODES, LIB_PATH, TBE_ERR_ARG, TbeError, _lib
+
+try:
+    from . import _lmcall
+except ImportError as e:
+    raise ImportError("_lmcall.so is missing, or built for another Python or torch: build it with "
+                      f"`python bwd_tbe_pooled_amd/build.py` ({e})") from e
 
 _P, _I64, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
 
@@ -39,7 +45,10 @@ class tbe_distill_desc(ctypes.Structure):
 
 
 def _declare(name, *args, restype=ctypes.c_int):
-    f = getattr(_lib, name)
+    try:
+        f = getattr(_lib, name)
+    except AttributeError as e:
+        raise ImportError(f"{LIB_PATH} has no language-model operators ({e})") from e
     f.restype, f.argtypes = restype, list(args)
     return f
 
