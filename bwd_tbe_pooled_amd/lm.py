@@ -77,6 +77,13 @@ _lmcall.bind(tuple(ctypes.cast(f, _P).value for f in (
     _expert_combine, _expert_combine_backward, _distill_forward, _distill_backward, _distill_step)))
 
 
+def _need_desc(desc, kind):
+    """Raise TypeError unless `desc` is a `kind`: the library reads the memory of a
+    description as what the call is for."""
+    if not isinstance(desc, kind):
+        raise TypeError(f"desc: expected {kind.__name__}, got {type(desc).__name__}")
+
+
 def _workspace(bytes_of, desc, where, device):
     n = int(bytes_of(desc.ref))
     if n == 0:
@@ -106,11 +113,14 @@ class TokenDesc(_LmDesc):
 
 def token_workspace(desc: TokenDesc, device="cuda"):
     """Workspace of tbe_token_backward."""
+    _need_desc(desc, TokenDesc)
     return _workspace(_token_workspace_bytes, desc, "tbe_token_workspace_bytes", device)
 
 
 def tbe_token_forward(desc: TokenDesc, W, ids, out, stream=None):
     """out[n] = scale * W[ids[n]]; zeros where the id is outside [0, V)."""
+    if type(desc) is not TokenDesc:
+        _need_desc(desc, TokenDesc)
     status = _lmcall.token_forward(desc.ref, W, ids, out, stream)
     if status:
         raise TbeError(status, "tbe_token_forward")
@@ -118,6 +128,8 @@ def tbe_token_forward(desc: TokenDesc, W, ids, out, stream=None):
 
 def tbe_token_backward(desc: TokenDesc, g, ids, gW, ws, stream=None):
     """gW[v] = scale * sum of g[n] over the tokens with ids[n] = v, all V rows."""
+    if type(desc) is not TokenDesc:
+        _need_desc(desc, TokenDesc)
     status = _lmcall.token_backward(desc.ref, g, ids, gW, ws, stream)
     if status:
         raise TbeError(status, "tbe_token_backward")
@@ -138,6 +150,7 @@ class ExpertPlan:
     """Device buffers of a plan: `offsets` [E+1], `order` [N*K], `slots` [N*K]."""
 
     def __init__(self, desc: ExpertDesc, device="cuda"):
+        _need_desc(desc, ExpertDesc)
         self.offsets = torch.empty(desc.E + 1, dtype=torch.int32, device=device)
         self.order = torch.empty(desc.M, dtype=torch.int32, device=device)
         self.slots = torch.empty(desc.M, dtype=torch.int32, device=device)
@@ -145,11 +158,14 @@ class ExpertPlan:
 
 def expert_workspace(desc: ExpertDesc, device="cuda"):
     """Workspace of tbe_expert_plan."""
+    _need_desc(desc, ExpertDesc)
     return _workspace(_expert_workspace_bytes, desc, "tbe_expert_workspace_bytes", device)
 
 
 def tbe_expert_plan(desc: ExpertDesc, ids, plan: ExpertPlan, ws, stream=None):
     """Sorts the assignments by expert into `plan` (dropped ones at the end)."""
+    if type(desc) is not ExpertDesc:
+        _need_desc(desc, ExpertDesc)
     status = _lmcall.expert_plan(desc.ref, ids, plan.offsets, plan.order, plan.slots, ws, stream)
     if status:
         raise TbeError(status, "tbe_expert_plan")
@@ -157,6 +173,8 @@ def tbe_expert_plan(desc: ExpertDesc, ids, plan: ExpertPlan, ws, stream=None):
 
 def tbe_expert_dispatch(desc: ExpertDesc, x, slots, xs, stream=None):
     """xs[place of (n, k)] = x[n]; zeros at the places of dropped assignments."""
+    if type(desc) is not ExpertDesc:
+        _need_desc(desc, ExpertDesc)
     status = _lmcall.expert_dispatch(desc.ref, x, slots, xs, stream)
     if status:
         raise TbeError(status, "tbe_expert_dispatch")
@@ -164,6 +182,8 @@ def tbe_expert_dispatch(desc: ExpertDesc, x, slots, xs, stream=None):
 
 def tbe_expert_dispatch_backward(desc: ExpertDesc, dxs, slots, dx, stream=None):
     """dx[n] = sum over kept k of dxs[place of (n, k)]."""
+    if type(desc) is not ExpertDesc:
+        _need_desc(desc, ExpertDesc)
     status = _lmcall.expert_dispatch_backward(desc.ref, dxs, slots, dx, stream)
     if status:
         raise TbeError(status, "tbe_expert_dispatch_backward")
@@ -171,6 +191,8 @@ def tbe_expert_dispatch_backward(desc: ExpertDesc, dxs, slots, dx, stream=None):
 
 def tbe_expert_combine(desc: ExpertDesc, ys, slots, w, out, stream=None):
     """out[n] = sum over kept k of w[n, k] * ys[place of (n, k)]."""
+    if type(desc) is not ExpertDesc:
+        _need_desc(desc, ExpertDesc)
     status = _lmcall.expert_combine(desc.ref, ys, slots, w, out, stream)
     if status:
         raise TbeError(status, "tbe_expert_combine")
@@ -179,6 +201,8 @@ def tbe_expert_combine(desc: ExpertDesc, ys, slots, w, out, stream=None):
 def tbe_expert_combine_backward(desc: ExpertDesc, dout, ys, slots, w, dys, dw, stream=None):
     """dys[place of (n, k)] = w[n, k] * dout[n], dw[n, k] = <dout[n], ys[place]>;
     zeros where the assignment is dropped. dys may be ys."""
+    if type(desc) is not ExpertDesc:
+        _need_desc(desc, ExpertDesc)
     status = _lmcall.expert_combine_backward(desc.ref, dout, ys, slots, w, dys, dw, stream)
     if status:
         raise TbeError(status, "tbe_expert_combine_backward")
@@ -197,11 +221,14 @@ class DistillDesc(_LmDesc):
 
 def distill_workspace(desc: DistillDesc, device="cuda"):
     """Workspace of tbe_distill_forward and tbe_distill_step."""
+    _need_desc(desc, DistillDesc)
     return _workspace(_distill_workspace_bytes, desc, "tbe_distill_workspace_bytes", device)
 
 
 def tbe_distill_forward(desc: DistillDesc, x, ids, t, loss, stats, ws, stream=None):
     """loss[n] = tau^2 KL(teacher || student) of row n; stats [N, 2] for the backward."""
+    if type(desc) is not DistillDesc:
+        _need_desc(desc, DistillDesc)
     status = _lmcall.distill_forward(desc.ref, x, ids, t, loss, stats, ws, stream)
     if status:
         raise TbeError(status, "tbe_distill_forward")
@@ -209,6 +236,8 @@ def tbe_distill_forward(desc: DistillDesc, x, ids, t, loss, stats, ws, stream=No
 
 def tbe_distill_backward(desc: DistillDesc, x, ids, t, stats, gl, gx, stream=None):
     """gx = gl * tau * (softmax(x / tau) - teacher). gx may be x."""
+    if type(desc) is not DistillDesc:
+        _need_desc(desc, DistillDesc)
     status = _lmcall.distill_backward(desc.ref, x, ids, t, stats, gl, gx, stream)
     if status:
         raise TbeError(status, "tbe_distill_backward")
@@ -216,6 +245,8 @@ def tbe_distill_backward(desc: DistillDesc, x, ids, t, stats, gl, gx, stream=Non
 
 def tbe_distill_step(desc: DistillDesc, x, ids, t, gl, loss, gx, ws, stream=None):
     """Loss and gradient in one call. gx may be x."""
+    if type(desc) is not DistillDesc:
+        _need_desc(desc, DistillDesc)
     status = _lmcall.distill_step(desc.ref, x, ids, t, gl, loss, gx, ws, stream)
     if status:
         raise TbeError(status, "tbe_distill_step")

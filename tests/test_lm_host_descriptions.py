@@ -1,0 +1,31 @@
+"""Language-model operators: a call takes its own operator's description alone.
+Refused on the host; no GPU is needed."""
+import pytest
+
+tbe = pytest.importorskip("bwd_tbe_pooled_amd", reason="libtbe.so not built")
+
+DESCS = {"token": tbe.TokenDesc(5, 40, 8), "expert": tbe.ExpertDesc(5, 2, 4, 8),
+         "distill": tbe.DistillDesc(5, 40, 8), "table": tbe.Desc(T=1, D=8, B=5, rows=[40], dtype="f32"),
+         "nothing": None}
+# call, its arguments beside the description
+CALLS = [("tbe_token_forward", 3), ("tbe_token_backward", 4), ("tbe_expert_plan", 3), ("tbe_expert_dispatch", 3),
+         ("tbe_expert_dispatch_backward", 3), ("tbe_expert_combine", 4), ("tbe_expert_combine_backward", 6),
+         ("tbe_distill_forward", 6), ("tbe_distill_backward", 6), ("tbe_distill_step", 7),
+         ("token_workspace", 0), ("expert_workspace", 0), ("distill_workspace", 0), ("ExpertPlan", 0)]
+
+
+@pytest.mark.parametrize("call,n", CALLS)
+def test_another_operators_description_is_refused(call, n):
+    operator = next(k for k in DESCS if k in call.lower())
+    kind = type(DESCS[operator]).__name__
+    for other, desc in DESCS.items():
+        if other != operator:
+            with pytest.raises(TypeError, match=f"desc: expected {kind}, got {type(desc).__name__}"):
+                getattr(tbe, call)(desc, *[None] * n)
+
+
+def test_a_subclass_is_taken():
+    class Mine(tbe.TokenDesc):
+        pass
+    with pytest.raises(TypeError, match="W: expected a torch.Tensor"):
+        tbe.tbe_token_forward(Mine(5, 40, 8), None, None, None)
