@@ -17,7 +17,7 @@ import ctypes
 
 import torch
 
-from . import DTYPE_CODES, LIB_PATH, TBE_ERR_ARG, TbeError, _lib
+from . import DTYPE_CODES, LIB_PATH, TBE_ERR_ARG, TBE_ERR_UNSUPPORTED, TbeError, _lib
 
 try:
     from . import _lmcall
@@ -94,7 +94,12 @@ def _workspace(bytes_of, desc, where, device):
 class _LmDesc:
     """Owns the C description `c`; `ref` is its address."""
 
-    def _own(self, c):
+    def _own(self, c_type, *values):
+        c = c_type(*values)
+        for (name, _), v in zip(c_type._fields_, values):
+            # ctypes keeps the low bits of a whole number that a field cannot hold
+            if isinstance(v, int) and getattr(c, name) != v:
+                raise TbeError(TBE_ERR_UNSUPPORTED, f"{type(self).__name__}: {name} = {v}")
         self.c = c
         self.ref = ctypes.addressof(c)
 
@@ -107,8 +112,8 @@ class TokenDesc(_LmDesc):
     def __init__(self, N: int, V: int, D: int, wdtype: str = "bf16", xdtype: str = "bf16",
                  idx64: bool = True, scale: float = 1.0):
         self.N, self.V, self.D = int(N), int(V), int(D)
-        self._own(tbe_token_desc(self.N, self.V, self.D, DTYPE_CODES[wdtype], DTYPE_CODES[xdtype],
-                                 int(bool(idx64)), float(scale)))
+        self._own(tbe_token_desc, self.N, self.V, self.D, DTYPE_CODES[wdtype], DTYPE_CODES[xdtype],
+                  int(bool(idx64)), float(scale))
 
 
 def token_workspace(desc: TokenDesc, device="cuda"):
@@ -142,8 +147,8 @@ class ExpertDesc(_LmDesc):
     def __init__(self, N: int, K: int, E: int, D: int, dtype: str = "bf16", idx64: bool = True):
         self.N, self.K, self.E, self.D = int(N), int(K), int(E), int(D)
         self.M = self.N * self.K
-        self._own(tbe_expert_desc(self.N, self.K, self.E, self.D, DTYPE_CODES[dtype],
-                                  int(bool(idx64))))
+        self._own(tbe_expert_desc, self.N, self.K, self.E, self.D, DTYPE_CODES[dtype],
+                  int(bool(idx64)))
 
 
 class ExpertPlan:
@@ -215,8 +220,8 @@ class DistillDesc(_LmDesc):
     def __init__(self, N: int, V: int, K: int, dtype: str = "bf16", tdtype: str = "f32",
                  idx64: bool = True, temperature: float = 1.0):
         self.N, self.V, self.K = int(N), int(V), int(K)
-        self._own(tbe_distill_desc(self.N, self.V, self.K, DTYPE_CODES[dtype], DTYPE_CODES[tdtype],
-                                   int(bool(idx64)), float(temperature)))
+        self._own(tbe_distill_desc, self.N, self.V, self.K, DTYPE_CODES[dtype], DTYPE_CODES[tdtype],
+                  int(bool(idx64)), float(temperature))
 
 
 def distill_workspace(desc: DistillDesc, device="cuda"):

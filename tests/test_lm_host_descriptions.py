@@ -29,3 +29,16 @@ def test_a_subclass_is_taken():
         pass
     with pytest.raises(TypeError, match="W: expected a torch.Tensor"):
         tbe.tbe_token_forward(Mine(5, 40, 8), None, None, None)
+
+
+@pytest.mark.parametrize("make", [
+    lambda big: tbe.TokenDesc(5, 40, big + 8), lambda big: tbe.ExpertDesc(5, big + 2, 4, 8),
+    lambda big: tbe.ExpertDesc(5, 2, big + 4, 8), lambda big: tbe.ExpertDesc(5, 2, 4, big + 8),
+    lambda big: tbe.DistillDesc(5, 40, big + 8), lambda big: tbe.TokenDesc(big * big + 5, 40, 8),
+    lambda big: tbe.DistillDesc(5, big * big + 40, 8)])
+def test_sizes_beyond_their_field_are_refused(make):
+    """2^32 + 8 columns are not 8 columns."""
+    with pytest.raises(tbe.TbeError, match="= [0-9]{10}") as e:
+        make(2 ** 32)
+    assert e.value.status == tbe.TBE_ERR_UNSUPPORTED
+    make(0)
