@@ -7,6 +7,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -55,6 +56,16 @@ at::ScalarType type_of(tbe_dtype t) {
 }
 at::ScalarType index_type(int32_t idx64) { return idx64 ? at::kLong : at::kInt; }
 
+// The device of the call's tensors, -1 before the first: a kernel may fault on
+// another device's memory, so all of them and the stream have to be of one.
+thread_local int call_device = -1;
+
+void on_call_device(const at::Tensor& x, const char* name) {
+  const int device = (int)x.get_device();
+  if (call_device < 0) call_device = device;
+  else if (device != call_device) refuse(name, "must be on the device of the call's other tensors");
+}
+
 const at::Tensor& tensor(PyObject* o, const char* name, at::ScalarType t) {
   if (!THPVariable_Check(o)) {
     PyErr_Format(PyExc_TypeError, "%s: expected a torch.Tensor, got %s", name, Py_TYPE(o)->tp_name);
@@ -67,6 +78,7 @@ const at::Tensor& tensor(PyObject* o, const char* name, at::ScalarType t) {
                  c10::toString(x.scalar_type()));
     throw Refused{};
   }
+  on_call_device(x, name);
   return x;
 }
 
@@ -113,18 +125,38 @@ struct Scratch {
 Scratch scratch(PyObject* o) {
   if (THPVariable_Check(o)) {
     const at::Tensor& x = THPVariable_Unpack(o);
-    if (x.is_cuda() && x.is_contiguous()) return {x.data_ptr(), x.nbytes()};
+    if (x.is_cuda() && x.is_contiguous()) {
+      on_call_device(x, "workspace");
+      return {x.data_ptr(), x.nbytes()};
+    }
   }
   refuse("workspace", "expected a contiguous device tensor");
 }
 
+// The stream's handle, after the call's tensors. A null handle is the default
+// stream of the current device.
 void* stream_of(PyObject* o) {
-  if (o == Py_None) return c10::hip::getCurrentHIPStream().stream();
+  constexpr const char* kOther = "must be of the tensors' device";
+  if (o == Py_None) {
+    const auto s = c10::hip::getCurrentHIPStream();
+    if (s.device_index() != call_device)
+      refuse("stream", "the current device must be the tensors' device");
+    return s.stream();
+  }
   PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
   if (!h) throw Refused{};
   void* s = PyLong_AsVoidPtr(h);
   Py_DECREF(h);
   if (PyErr_Occurred()) throw Refused{};
+  if (PyObject* d = PyObject_GetAttrString(o, "device_index")) {
+    const long device = PyLong_AsLong(d);
+    Py_DECREF(d);
+    if (PyErr_Occurred()) throw Refused{};
+    if (device != call_device) refuse("stream", kOther);
+  } else {
+    PyErr_Clear();  // a handle alone
+  }
+  if (!s && c10::hip::current_device() != call_device) refuse("stream", kOther);
   return s;
 }
 
@@ -145,6 +177,7 @@ PyObject* call(PyObject* const* a, Py_ssize_t n, F f) {
     PyErr_Format(PyExc_TypeError, "expected %d arguments, got %zd", N, n);
     return nullptr;
   }
+  call_device = -1;
   try {
     return PyLong_FromLong(f(a));
   } catch (const Refused&) {
