@@ -690,7 +690,7 @@ Args make_args(const tbe_distill_desc& d, const void* ids, const void* t) {
   g.N = d.N;
   g.V = d.V;
   g.tau = d.temperature;
-  g.a = (float)(1.4426950408889634 / (double)d.temperature);
+  g.a = distill_factor(d.temperature);
   return g;
 }
 

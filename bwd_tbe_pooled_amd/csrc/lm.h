@@ -63,6 +63,10 @@ hipError_t launch_token_backward(const tbe_token_desc& d, const TokenLayout& L, 
                                  int64_t ldg, const void* ids, void* gW, int64_t ldgw, void* ws,
                                  hipStream_t s);
 
+// log2(e) / temperature: the kernels' powers are of 2.
+inline float distill_factor(float temperature) {
+  return (float)(1.4426950408889634 / (double)temperature);
+}
 hipError_t launch_distill_forward(const tbe_distill_desc& d, const void* x, int64_t ldx,
                                   const void* ids, const void* t, float* loss, float* stats,
                                   void* ws, hipStream_t s);

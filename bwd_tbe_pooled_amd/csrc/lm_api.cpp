@@ -42,6 +42,8 @@ tbe_status check(const tbe_distill_desc* d) {
   if (!d || d->N < 0 || d->V < 1 || d->K < 1 || !idx_ok(d->idx64)) return TBE_ERR_ARG;
   if (!(d->temperature > 0.f) || !std::isfinite(d->temperature)) return TBE_ERR_ARG;
   if (!type_ok(d->dtype) || !type_ok(d->tdtype)) return TBE_ERR_UNSUPPORTED;
+  // below 4.24e-39 (a subnormal number) the powers' factor is no float32
+  if (!std::isfinite(distill_factor(d->temperature))) return TBE_ERR_UNSUPPORTED;
   if (d->N >= kI32Lim || d->V >= kI32Lim || d->K > 1024) return TBE_ERR_UNSUPPORTED;
   return TBE_OK;
 }

@@ -134,7 +134,8 @@ tbe_status tbe_expert_combine_backward(const tbe_expert_desc* desc, const void* 
  * same id may occur more than once in a row. Logits of -inf have q = 0 (a
  * teacher's entry there with p > 0 makes the loss +inf); a row with a NaN or
  * +inf logit, or none but -inf, gives NaN.
- * 1 <= V < 2^31 - 1, 1 <= K <= 1024, tau finite and > 0. */
+ * 1 <= V < 2^31 - 1, 1 <= K <= 1024, tau finite and > 0 (TBE_ERR_UNSUPPORTED
+ * below 4.24e-39, where log2(e) / tau is no float32). */
 typedef struct {
     int64_t N;            /* rows, >= 0 */
     int64_t V;            /* vocabulary */

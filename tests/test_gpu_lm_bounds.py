@@ -147,3 +147,25 @@ def test_statistics(x, V, tau):
     tbe.tbe_distill_backward(desc, xs, ids, ts, own, gl, gx)
     for i, kind in enumerate(kinds):
         close(gx[i], want.gx[i], want.bg[i], x, f"gradient, {kind}")
+
+
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("tau", [5e-39, 2.0 ** -126, 2.0 ** -100, 2.0 ** -20, 2.0 ** 20, 2.0 ** 100, 3e38])
+def test_temperatures(tau, x):
+    """Logits and gradients in units of a very low or high temperature. (The loss
+    is in units of its square, 0 or inf in float32.)"""
+    say("distill temperature", tau, x)
+    tbe = lib()
+    g = gen(7)
+    for N, V in ((3, 700), (40, 5003)):
+        xs = (tau * 0.2 * torch.randn(N, V, generator=g)).to(DT[x]).cuda()
+        ids = torch.stack([torch.randperm(V, generator=g)[:5] for _ in range(N)]).cuda()
+        ts = (tau * 0.2 * torch.randn(N, 5, generator=g)).cuda()
+        gl = (0.2 / tau * torch.randn(N, generator=g)).cuda()
+        tau32 = torch.tensor(tau).to(F64).item()
+        want = Ref(xs, ids, ts, tau32, gl)
+        desc = tbe.DistillDesc(N, V, 5, dtype=x, temperature=tau)
+        outs = run_distill(tbe, desc, xs, ids, ts, gl)
+        for loss, grad in (outs[:2], outs[2:]):
+            close(loss, want.loss.float(), want.bl, "f32", "loss")
+            close(grad, want.gx, want.bg, x, "gradient")

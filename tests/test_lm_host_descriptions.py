@@ -42,3 +42,13 @@ def test_sizes_beyond_their_field_are_refused(make):
         make(2 ** 32)
     assert e.value.status == tbe.TBE_ERR_UNSUPPORTED
     make(0)
+
+
+def test_temperatures_without_a_factor_are_refused():
+    """log2(e) / temperature has to be a float32."""
+    from bwd_tbe_pooled_amd import lm
+    for t, want in ((1e-45, tbe.TBE_ERR_UNSUPPORTED), (4.2e-39, tbe.TBE_ERR_UNSUPPORTED), (4.3e-39, tbe.TBE_OK),
+                    (3.4e38, tbe.TBE_OK), (1e-46, tbe.TBE_ERR_ARG)):   # (1e-46 is 0 in float32)
+        d = tbe.DistillDesc(0, 5, 2, temperature=t)
+        assert lm._distill_backward(d.ref, None, 5, None, None, None, None, None, 5, None) == want, t
+        assert (lm._distill_workspace_bytes(d.ref) > 0) == (want == tbe.TBE_OK)
