@@ -7,9 +7,12 @@
   distill  tbe_distill_forward, tbe_distill_backward, tbe_distill_step: the
            loss against a teacher's top logits, and its gradient
 
-Argument marshalling only, as in the package's other functions. Matrices are
-2-D device tensors with unit column stride and any row stride (an output's at
-least its width); ids and per-row vectors are contiguous.
+Matrices are 2-D device tensors with unit column stride and any row stride (an
+output's at least its width); ids and per-row vectors are contiguous; all are on
+one device, the stream's. The checks of a call's tensors and the call itself are
+compiled (csrc/lm_call.cpp); the functions here check the description's kind and
+turn a status into an error. The ctypes declarations give the descriptions their
+workspace sizes, the compiled calls their addresses and tests the plain C ABI.
 """
 from __future__ import annotations
 

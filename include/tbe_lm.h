@@ -147,7 +147,9 @@ typedef struct {
 } tbe_distill_desc;
 
 /* Bytes of the workspace of the forward and the step (0 on a bad
- * description), as above. */
+ * description), as above. Both calls require it; the kernels of this version
+ * need no scratch memory and leave it as it is, so its size is one alignment
+ * unit whatever the description. */
 size_t tbe_distill_workspace_bytes(const tbe_distill_desc* desc);
 
 /* x: device [N, V]. ids, t: device [N, K], dense. loss: device float32 [N],
