@@ -394,17 +394,21 @@ def exported_symbols() -> list:
             "tbe_expert_workspace_bytes", "tbe_expert_plan", "tbe_expert_dispatch",
             "tbe_expert_dispatch_backward", "tbe_expert_combine", "tbe_expert_combine_backward",
             "tbe_distill_workspace_bytes", "tbe_distill_forward", "tbe_distill_backward",
-            "tbe_distill_step"]
+            "tbe_distill_step",
+            "tbe_norm_forward", "tbe_norm_workspace_bytes", "tbe_norm_backward",
+            "tbe_ffn_workspace_bytes", "tbe_ffn_forward", "tbe_ffn_backward", "tbe_adamw_step"]
 
 
 # --- language-model operators (include/tbe_lm.h) ---------------------------------------
 # Loaded at first use: they need _lmcall.so, an extension for one Python and one
 # torch, where the calls above need libtbe.so alone.
-_LM_NAMES = ("DistillDesc", "ExpertDesc", "ExpertPlan", "TokenDesc", "distill_workspace",
-             "expert_workspace", "tbe_distill_backward", "tbe_distill_forward", "tbe_distill_step",
+_LM_NAMES = ("AdamWDesc", "AdamWState", "DistillDesc", "ExpertDesc", "ExpertPlan", "FfnDesc", "NormDesc",
+             "TokenDesc", "distill_workspace", "expert_workspace", "ffn_workspace", "norm_workspace",
+             "tbe_adamw_step", "tbe_distill_backward", "tbe_distill_forward", "tbe_distill_step",
              "tbe_expert_combine", "tbe_expert_combine_backward", "tbe_expert_dispatch",
-             "tbe_expert_dispatch_backward", "tbe_expert_plan", "tbe_token_backward",
-             "tbe_token_forward", "token_workspace")
+             "tbe_expert_dispatch_backward", "tbe_expert_plan", "tbe_ffn_backward", "tbe_ffn_forward",
+             "tbe_norm_backward", "tbe_norm_forward", "tbe_token_backward", "tbe_token_forward",
+             "token_workspace")
 
 
 def __getattr__(name):

@@ -30,7 +30,8 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall",
 
 SOURCES = ["api.cpp", "util.hip", "forward.hip", "hot_rows.hip", "sort.hip", "rle_route.hip",
            "backward.hip", "hot_backward.hip", "probe.hip", "small_table.hip",
-           "lm_api.cpp", "token.hip", "expert.hip", "distill.hip"]
+           "lm_api.cpp", "token.hip", "expert.hip", "distill.hip", "norm.hip", "ffn.hip",
+           "adamw.hip"]
 
 
 def _compile(src: str) -> str:

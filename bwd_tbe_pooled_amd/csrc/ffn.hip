@@ -1,0 +1,331 @@
+// The experts' gated feed-forward products and their gradients.
+//
+//   forward   h = act(xs gate^T) * (xs up^T)      one kernel: a tile holds the same
+//                                                 columns of both products
+//             ys = h down^T
+//   backward  dh = dys down, from which the same kernel forms the gradients of the
+//                            two products, and h again, from the kept products
+//             dxs = dg gate + du up               one sum over 2 F
+//             dgate = dg^T xs, dup = du^T xs, ddown = dys^T h       one kernel
+//
+// A workgroup finds its expert and rows from the offsets by itself, so nothing
+// waits for the host; workgroups beyond the last tile end at once. A tile's rows
+// are one expert's: rows behind its end repeat its last row and are not stored.
+#include <algorithm>
+
+#include "ffn_tile.h"
+
+namespace tbe {
+namespace {
+
+enum Product { Up, Down, Dh, Dx, Dw };
+
+struct Args {
+  const int32_t* offsets;
+  int32_t M, E, D, F;
+  int32_t act;
+  int32_t nt;                      // blocks of columns (Dw: unused)
+  int64_t tiles;
+  const void* a; int64_t lda;      // rows: xs, h, dys, or the gradients of g and u
+  tbe_stack b0, b1;                // matrices: gate and up, or down
+  const void* pre; int64_t ldpre;  // Dh: the kept products
+  void* c; int64_t ldc;            // rows written: h, ys, dxs
+  void* c2; int64_t ldc2;          // Up: pre or NULL; Dh: the gradients of g and u
+  int64_t half;                    // columns from g's gradient to u's
+  // Dw: dys, xs and the three results
+  const void* dys; int64_t lddys;
+  const void* xs; int64_t ldxs;
+  const void* h; int64_t ldh;
+  tbe_stack o0, o1, o2;
+};
+
+// The activation and its derivative.
+template <typename T>
+__device__ __forceinline__ void activate(int32_t act, float g, float& a, float& da) {
+  if (act == TBE_ACT_SILU) {
+    const float s = 1.f / (1.f + (sizeof(T) == 4 ? expf(-g) : __expf(-g)));
+    a = g * s;
+    da = s * fmaf(g, 1.f - s, 1.f);
+  } else {
+    const float cdf = 0.5f * (1.f + erff(g * 0.70710678f));
+    a = g * cdf;
+    da = fmaf(g * 0.39894228f, sizeof(T) == 4 ? expf(-0.5f * g * g) : __expf(-0.5f * g * g), cdf);
+  }
+}
+
+// Up to four neighbouring elements of a row.
+template <typename T>
+__device__ __forceinline__ void store4(T* p, int32_t n, const float (&f)[4]) {
+  if (n >= 4) {
+    store_pack<T, 4>(p, narrow<T, 4>(f));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < n) p[j] = round_to<T>(f[j]);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, int32_t n, float (&f)[4]) {
+  if (n >= 4) {
+    widen<T, 4>(load_pack<T, 4>(p), f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = j < n ? to_float(p[j]) : 0.f;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ const T* matrix(const tbe_stack& m, int32_t e) {
+  return static_cast<const T*>(m.data) + (int64_t)e * m.stride;
+}
+
+template <typename T, Product P, class S, bool VEC>
+__global__ __launch_bounds__(S::NT) void ffn_kernel(Args g) {
+  __shared__ __attribute__((aligned(16))) char lds[2 * S::AREA];
+  const int64_t tile = xcd_logical_block(g.tiles);
+  if (tile < 0) return;
+  const int wave = wave_index(), lane = lane_id();
+  const int wm = wave / S::WN, wn = wave % S::WN;
+  f32x4 acc[S::MF][S::NF];
+#pragma unroll
+  for (int i = 0; i < S::MF; ++i)
+#pragma unroll
+    for (int j = 0; j < S::NF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  if constexpr (P == Dw) {
+    // tiles of one expert: gate's, up's, down's
+    const int32_t ft = (g.F + S::BM - 1) / S::BM, dt = (g.D + S::BN - 1) / S::BN;
+    const int32_t dt2 = (g.D + S::BM - 1) / S::BM, ft2 = (g.F + S::BN - 1) / S::BN;
+    const int32_t each = ft * dt, per = 2 * each + dt2 * ft2;
+    Span s;
+    expert_rows(g.offsets, (int32_t)(tile / per), g.M, s);
+    const int32_t at = (int32_t)(tile % per);
+    const int which = at < each ? 0 : at < 2 * each ? 1 : 2;
+    const int32_t in = at - which * each;
+    const int32_t across = which == 2 ? ft2 : dt;
+    const int32_t m0 = in / across * S::BM, n0 = in % across * S::BN;
+    const int32_t rows = which == 2 ? g.D : g.F, cols = which == 2 ? g.F : g.D;
+    const T* a = static_cast<const T*>(which == 2 ? g.dys : g.a) + (which == 1 ? g.half : 0);
+    const T* b = static_cast<const T*>(which == 2 ? g.h : g.xs);
+    const int64_t lda = which == 2 ? g.lddys : g.lda, ldb = which == 2 ? g.ldh : g.ldxs;
+    Operand<T, Across, S::BM, S::NT, VEC> oa;
+    Operand<T, Across, S::BN, S::NT, VEC> ob;
+    oa.start(rows - m0, lda, [&](int) { return a + (int64_t)s.first * lda + m0; });
+    ob.start(cols - n0, ldb, [&](int) { return b + (int64_t)s.first * ldb + n0; });
+    multiply<T, S>(acc, oa, ob, s.end - s.first, lds, [&](int j) { return (wn * S::NF + j) * 16; });
+    const tbe_stack& o = which == 0 ? g.o0 : which == 1 ? g.o1 : g.o2;
+    T* out = static_cast<T*>(o.data) + (int64_t)s.e * o.stride;
+#pragma unroll
+    for (int i = 0; i < S::MF; ++i) {
+      const int32_t m = m0 + (wm * S::MF + i) * 16 + lane % 16;
+      if (m >= rows) continue;
+#pragma unroll
+      for (int j = 0; j < S::NF; ++j) {
+        const int32_t n = n0 + (wn * S::NF + j) * 16 + lane / 16 * 4;
+        const float f[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+        store4<T>(out + (int64_t)m * o.ld + n, cols - n, f);
+      }
+    }
+    return;
+  } else {
+    Span s;
+    if (!find_block<S::BM>(g.offsets, g.E, g.M, g.nt, (int32_t)tile, s)) return;
+    const int32_t m0 = s.first + s.place % s.tiles * S::BM;
+    // columns of a tile: of Up's two products half each
+    constexpr int BN = P == Up ? S::BN / 2 : S::BN;
+    const int32_t n0 = s.place / s.tiles * BN;
+    const int32_t N = P == Up || P == Dh ? g.F : g.D;
+    const T* a = static_cast<const T*>(g.a);
+    const int32_t last = s.end - 1;
+    Operand<T, Along, S::BM, S::NT, VEC> oa;
+    oa.start(S::BM, g.lda, [&](int r) { return a + (int64_t)min(m0 + r, last) * g.lda; });
+    constexpr int HALF = S::NF / 2;
+    if constexpr (P == Up) {
+      static_assert(S::NF % 2 == 0, "both products in one wave");
+      const T *b0 = matrix<T>(g.b0, s.e), *b1 = matrix<T>(g.b1, s.e);
+      Operand<T, Along, S::BN, S::NT, VEC> ob;
+      ob.start(S::BN, 0, [&](int r) {
+        const int64_t n = min(n0 + (r < BN ? r : r - BN), N - 1);
+        return r < BN ? b0 + n * g.b0.ld : b1 + n * g.b1.ld;
+      });
+      multiply<T, S>(acc, oa, ob, g.D, lds, [&](int j) {
+        return j < HALF ? (wn * HALF + j) * 16 : BN + (wn * HALF + j - HALF) * 16;
+      });
+    } else if constexpr (P == Down) {
+      const T* b0 = matrix<T>(g.b0, s.e);
+      Operand<T, Along, S::BN, S::NT, VEC> ob;
+      ob.start(S::BN, 0, [&](int r) { return b0 + (int64_t)min(n0 + r, N - 1) * g.b0.ld; });
+      multiply<T, S>(acc, oa, ob, g.F, lds, [&](int j) { return (wn * S::NF + j) * 16; });
+    } else {
+      const T* b0 = matrix<T>(g.b0, s.e);
+      Operand<T, Across, S::BN, S::NT, VEC> ob;
+      ob.start(N - n0, g.b0.ld, [&](int) { return b0 + n0; });
+      auto row_b = [&](int j) { return (wn * S::NF + j) * 16; };
+      multiply<T, S>(acc, oa, ob, P == Dh ? g.D : g.F, lds, row_b);
+      if constexpr (P == Dx) {
+        const T* b1 = matrix<T>(g.b1, s.e);
+        oa.start(S::BM, g.lda, [&](int r) { return a + g.half + (int64_t)min(m0 + r, last) * g.lda; });
+        ob.start(N - n0, g.b1.ld, [&](int) { return b1 + n0; });
+        multiply<T, S>(acc, oa, ob, g.F, lds, row_b);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < S::MF; ++i) {
+      const int32_t m = m0 + (wm * S::MF + i) * 16 + lane % 16;
+      if (m >= s.end) continue;
+      T* c = static_cast<T*>(g.c) + (int64_t)m * g.ldc;
+      T* c2 = static_cast<T*>(g.c2) + (int64_t)m * g.ldc2;
+#pragma unroll
+      for (int j = 0; j < (P == Up ? HALF : S::NF); ++j) {
+        const int32_t n = n0 + (wn * (P == Up ? HALF : S::NF) + j) * 16 + lane / 16 * 4;
+        if (n >= N) continue;
+        float f[4], u[4], v[4];
+        if constexpr (P == Up) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float da;
+            u[q] = acc[i][j][q];
+            v[q] = acc[i][j + HALF][q];
+            activate<T>(g.act, u[q], f[q], da);
+            f[q] *= v[q];
+          }
+          if (g.c2) {
+            store4<T>(c2 + n, N - n, u);
+            store4<T>(c2 + N + n, N - n, v);
+          }
+        } else if constexpr (P == Dh) {
+          const T* pre = static_cast<const T*>(g.pre) + (int64_t)m * g.ldpre;
+          load4<T>(pre + n, N - n, u);
+          load4<T>(pre + N + n, N - n, v);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float dh = acc[i][j][q];
+            float x, da;
+            activate<T>(g.act, u[q], x, da);
+            f[q] = x * v[q];
+            u[q] = dh * v[q] * da;
+            v[q] = dh * x;
+          }
+          store4<T>(c2 + n, N - n, u);
+          store4<T>(c2 + g.half + n, N - n, v);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) f[q] = acc[i][j][q];
+        }
+        store4<T>(c + n, N - n, f);
+      }
+    }
+  }
+}
+
+int64_t blocks_of(int64_t n, int64_t b) { return (n + b - 1) / b; }
+
+// Launches one product with tiles of shape S.
+template <typename T, Product P, class S>
+hipError_t launch(Args g, bool vec, hipStream_t s) {
+  if constexpr (P == Dw) {
+    g.tiles = (int64_t)g.E * (2 * blocks_of(g.F, S::BM) * blocks_of(g.D, S::BN) +
+                              blocks_of(g.D, S::BM) * blocks_of(g.F, S::BN));
+  } else {
+    constexpr int BN = P == Up ? S::BN / 2 : S::BN;
+    g.nt = (int32_t)blocks_of(P == Up || P == Dh ? g.F : g.D, BN);
+    // every expert may end in a part of a block
+    g.tiles = (g.M / S::BM + std::min(g.E, g.M)) * (int64_t)g.nt;
+  }
+  const unsigned grid = (unsigned)xcd_grid(g.tiles);
+  if (vec) ffn_kernel<T, P, S, true><<<grid, S::NT, 0, s>>>(g);
+  else ffn_kernel<T, P, S, false><<<grid, S::NT, 0, s>>>(g);
+  return hipGetLastError();
+}
+
+// Whether all pieces of 16 bytes lie whole and aligned in their matrices.
+struct Aligned {
+  size_t size;
+  bool ok = true;
+  void rows(const void* p, int64_t ld) {
+    ok = ok && reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0;
+  }
+  void stack(const tbe_stack& m) {
+    rows(m.data, m.ld);
+    ok = ok && m.stride * size % 16 == 0;
+  }
+};
+
+using Middle = Shape<2, 2, 4, 4>;   // 128 x 128
+
+}  // namespace
+
+FfnLayout ffn_layout(const tbe_ffn_desc& d) {
+  const size_t size = d.dtype == TBE_F32 ? 4 : 2;
+  auto pad = [](size_t n) { return (n + 255) / 256 * 256; };
+  FfnLayout L;
+  L.ld = (d.F + 7) / 8 * 8;
+  L.h = 0;
+  L.dgu = pad((size_t)d.M * L.ld * size);
+  L.total = L.dgu + pad((size_t)d.M * 2 * L.ld * size) + 256;
+  return L;
+}
+
+hipError_t launch_ffn_forward(const tbe_ffn_desc& d, const FfnForward& a, hipStream_t s) {
+  const FfnLayout L = ffn_layout(d);
+  return with_type(d.dtype, [&](auto t) {
+    using T = decltype(t);
+    Aligned al{sizeof(T)};
+    al.rows(a.xs, a.ldxs);
+    al.rows(nullptr, d.D);
+    al.rows(nullptr, d.F);
+    for (const tbe_stack* m : {&a.gate, &a.up, &a.down}) al.stack(*m);
+    Args g = {};
+    g.offsets = a.offsets;
+    g.M = (int32_t)d.M; g.E = d.E; g.D = d.D; g.F = d.F; g.act = d.act;
+    g.a = a.xs; g.lda = a.ldxs;
+    g.b0 = a.gate; g.b1 = a.up;
+    g.c = a.ws + L.h; g.ldc = L.ld;
+    g.c2 = a.pre; g.ldc2 = a.ldpre;
+    hipError_t e = launch<T, Up, Middle>(g, al.ok, s);
+    if (e != hipSuccess) return e;
+    g.a = a.ws + L.h; g.lda = L.ld;
+    g.b0 = a.down;
+    g.c = a.ys; g.ldc = a.ldys;
+    return launch<T, Down, Middle>(g, al.ok, s);
+  });
+}
+
+hipError_t launch_ffn_backward(const tbe_ffn_desc& d, const FfnBackward& a, hipStream_t s) {
+  const FfnLayout L = ffn_layout(d);
+  return with_type(d.dtype, [&](auto t) {
+    using T = decltype(t);
+    Aligned al{sizeof(T)};
+    al.rows(a.xs, a.ldxs);
+    al.rows(a.dys, a.lddys);
+    al.rows(nullptr, d.D);
+    al.rows(nullptr, d.F);
+    for (const tbe_stack* m : {&a.gate, &a.up, &a.down}) al.stack(*m);
+    Args g = {};
+    g.offsets = a.offsets;
+    g.M = (int32_t)d.M; g.E = d.E; g.D = d.D; g.F = d.F; g.act = d.act;
+    g.half = L.ld;
+    if (d.M > 0) {
+      g.a = a.dys; g.lda = a.lddys;
+      g.b0 = a.down;
+      g.pre = a.pre; g.ldpre = a.ldpre;
+      g.c = a.ws + L.h; g.ldc = L.ld;
+      g.c2 = a.ws + L.dgu; g.ldc2 = 2 * L.ld;
+      hipError_t e = launch<T, Dh, Middle>(g, al.ok, s);
+      if (e != hipSuccess) return e;
+      g.a = a.ws + L.dgu; g.lda = 2 * L.ld;
+      g.b0 = a.gate; g.b1 = a.up;
+      g.c = a.dxs; g.ldc = a.lddxs;
+      e = launch<T, Dx, Middle>(g, al.ok, s);
+      if (e != hipSuccess) return e;
+    }
+    g.a = a.ws + L.dgu; g.lda = 2 * L.ld;
+    g.dys = a.dys; g.lddys = a.lddys;
+    g.xs = a.xs; g.ldxs = a.ldxs;
+    g.h = a.ws + L.h; g.ldh = L.ld;
+    g.o0 = a.dgate; g.o1 = a.dup; g.o2 = a.ddown;
+    return launch<T, Dw, Middle>(g, al.ok, s);
+  });
+}
+
+}  // namespace tbe

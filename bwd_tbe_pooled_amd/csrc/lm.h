@@ -78,4 +78,45 @@ hipError_t launch_distill_step(const tbe_distill_desc& d, const void* x, int64_t
                                void* gx, int64_t ldgx, void* ws, hipStream_t s);
 size_t distill_workspace(const tbe_distill_desc& d);
 
+// Layer norm. The backward's workgroups leave a partial row of dw and db each.
+int32_t norm_partials(const tbe_norm_desc& d);
+hipError_t launch_norm_forward(const tbe_norm_desc& d, const void* x, int64_t ldx, const void* w,
+                               const void* b, void* y, int64_t ldy, float* stats, hipStream_t s);
+hipError_t launch_norm_backward(const tbe_norm_desc& d, const void* dy, int64_t lddy, const void* x,
+                                int64_t ldx, const void* w, const float* stats, void* dx,
+                                int64_t lddx, void* dw, void* db, float* parts, hipStream_t s);
+
+// Experts' products: workspace regions, byte offsets.
+struct FfnLayout {
+  int64_t ld;     // elements of a row of h; a row of the gradients of g and u has two of them
+  size_t h;       // [M, ld]
+  size_t dgu;     // [M, 2 ld], backward only
+  size_t total;
+};
+FfnLayout ffn_layout(const tbe_ffn_desc& d);
+struct FfnForward {
+  const void* xs; int64_t ldxs;
+  const int32_t* offsets;
+  tbe_stack gate, up, down;
+  void* pre; int64_t ldpre;
+  void* ys; int64_t ldys;
+  char* ws;
+};
+struct FfnBackward {
+  const void* dys; int64_t lddys;
+  const void* xs; int64_t ldxs;
+  const int32_t* offsets;
+  tbe_stack gate, up, down;
+  const void* pre; int64_t ldpre;
+  void* dxs; int64_t lddxs;
+  tbe_stack dgate, dup, ddown;
+  char* ws;
+};
+hipError_t launch_ffn_forward(const tbe_ffn_desc& d, const FfnForward& a, hipStream_t s);
+hipError_t launch_ffn_backward(const tbe_ffn_desc& d, const FfnBackward& a, hipStream_t s);
+
+constexpr int kAdamBlock = 256;   // elements that share a scale of an 8-bit moment
+hipError_t launch_adamw(const tbe_adamw_desc& d, const tbe_adamw_tensor* tensors, int64_t count,
+                        const int64_t* step, const float* lr, const float* scale, hipStream_t s);
+
 }  // namespace tbe

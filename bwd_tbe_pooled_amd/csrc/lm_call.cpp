@@ -30,6 +30,11 @@ struct Entry {
   decltype(&tbe_distill_forward) distill_forward;
   decltype(&tbe_distill_backward) distill_backward;
   decltype(&tbe_distill_step) distill_step;
+  decltype(&tbe_norm_forward) norm_forward;
+  decltype(&tbe_norm_backward) norm_backward;
+  decltype(&tbe_ffn_forward) ffn_forward;
+  decltype(&tbe_ffn_backward) ffn_backward;
+  decltype(&tbe_adamw_step) adamw_step;
 } lib;
 
 // A refused argument; the Python error is set.
@@ -46,6 +51,7 @@ const char* type_name(at::ScalarType t) {
     case at::kHalf: return "torch.float16";
     case at::kBFloat16: return "torch.bfloat16";
     case at::kInt: return "torch.int32";
+    case at::kFloat8_e4m3fn: return "torch.float8_e4m3fn";
     default: return "torch.int64";
   }
 }
@@ -328,6 +334,156 @@ PyObject* distill_step(PyObject*, Args args, Py_ssize_t n) {
   });
 }
 
+// A vector of the norm's weights' type, or NULL for None.
+void* weight_vec(PyObject* o, const char* name, const tbe_norm_desc& d) {
+  return o == Py_None ? nullptr : vec(o, name, type_of(d.wdtype), d.D);
+}
+
+PyObject* norm_forward(PyObject*, Args args, Py_ssize_t n) {
+  return call<7>(args, n, [](Args a) {
+    const auto& d = desc<tbe_norm_desc>(a[0]);
+    const Mat x = mat(a[1], "x", type_of(d.dtype), d.N, d.D);
+    const void* w = weight_vec(a[2], "w", d);
+    const void* b = weight_vec(a[3], "b", d);
+    const Mat y = mat(a[4], "y", type_of(d.dtype), d.N, d.D, true);
+    auto* stats = static_cast<float*>(vec(a[5], "stats", at::kFloat, d.N, 2));
+    return lib.norm_forward(&d, x.p, x.ld, w, b, y.p, y.ld, stats, stream_of(a[6]));
+  });
+}
+
+PyObject* norm_backward(PyObject*, Args args, Py_ssize_t n) {
+  return call<10>(args, n, [](Args a) {
+    const auto& d = desc<tbe_norm_desc>(a[0]);
+    const Mat dy = mat(a[1], "dy", type_of(d.dtype), d.N, d.D);
+    const Mat x = mat(a[2], "x", type_of(d.dtype), d.N, d.D);
+    const void* w = weight_vec(a[3], "w", d);
+    auto* stats = static_cast<const float*>(vec(a[4], "stats", at::kFloat, d.N, 2));
+    const Mat dx = mat(a[5], "dx", type_of(d.dtype), d.N, d.D, true);
+    void* dw = weight_vec(a[6], "dw", d);
+    void* db = weight_vec(a[7], "db", d);
+    const Scratch ws = scratch(a[8]);
+    return lib.norm_backward(&d, dy.p, dy.ld, x.p, x.ld, w, stats, dx.p, dx.ld, dw, db, ws.p,
+                             ws.bytes, stream_of(a[9]));
+  });
+}
+
+// E matrices of rows x cols with unit column stride.
+tbe_stack stack(PyObject* o, const char* name, at::ScalarType t, int64_t E, int64_t rows,
+                int64_t cols, bool out = false) {
+  const at::Tensor& x = tensor(o, name, t);
+  const auto size = x.sizes();
+  if (size.size() != 3 || size[0] != E || size[1] != rows || size[2] != cols) {
+    char s[96];
+    std::snprintf(s, sizeof s, "expected shape (%lld, %lld, %lld)", (long long)E, (long long)rows,
+                  (long long)cols);
+    refuse(name, s);
+  }
+  const auto stride = x.strides();
+  if (stride[2] != 1 && cols > 1) refuse(name, "columns must be contiguous");
+  const int64_t ld = rows <= 1 ? cols : stride[1];
+  const int64_t each = E <= 1 ? rows * ld : stride[0];
+  if (out && (ld < cols || each / ld < rows)) refuse(name, "rows of an output must not overlap");
+  return {x.data_ptr(), ld, each};
+}
+
+const int32_t* offsets_of(PyObject* o, const tbe_ffn_desc& d) {
+  return static_cast<const int32_t*>(vec(o, "offsets", at::kInt, (int64_t)d.E + 1));
+}
+
+PyObject* ffn_forward(PyObject*, Args args, Py_ssize_t n) {
+  return call<10>(args, n, [](Args a) {
+    const auto& d = desc<tbe_ffn_desc>(a[0]);
+    const at::ScalarType t = type_of(d.dtype);
+    const Mat xs = mat(a[1], "xs", t, d.M, d.D);
+    const int32_t* offsets = offsets_of(a[2], d);
+    const tbe_stack gate = stack(a[3], "gate", t, d.E, d.F, d.D);
+    const tbe_stack up = stack(a[4], "up", t, d.E, d.F, d.D);
+    const tbe_stack down = stack(a[5], "down", t, d.E, d.D, d.F);
+    Mat pre{nullptr, 0};
+    if (a[6] != Py_None) pre = mat(a[6], "pre", t, d.M, 2 * (int64_t)d.F, true);
+    const Mat ys = mat(a[7], "ys", t, d.M, d.D, true);
+    const Scratch ws = scratch(a[8]);
+    return lib.ffn_forward(&d, xs.p, xs.ld, offsets, &gate, &up, &down, pre.p, pre.ld, ys.p, ys.ld,
+                           ws.p, ws.bytes, stream_of(a[9]));
+  });
+}
+
+PyObject* ffn_backward(PyObject*, Args args, Py_ssize_t n) {
+  return call<14>(args, n, [](Args a) {
+    const auto& d = desc<tbe_ffn_desc>(a[0]);
+    const at::ScalarType t = type_of(d.dtype);
+    const Mat dys = mat(a[1], "dys", t, d.M, d.D);
+    const Mat xs = mat(a[2], "xs", t, d.M, d.D);
+    const int32_t* offsets = offsets_of(a[3], d);
+    const tbe_stack gate = stack(a[4], "gate", t, d.E, d.F, d.D);
+    const tbe_stack up = stack(a[5], "up", t, d.E, d.F, d.D);
+    const tbe_stack down = stack(a[6], "down", t, d.E, d.D, d.F);
+    const Mat pre = mat(a[7], "pre", t, d.M, 2 * (int64_t)d.F);
+    const Mat dxs = mat(a[8], "dxs", t, d.M, d.D, true);
+    const tbe_stack dgate = stack(a[9], "dgate", t, d.E, d.F, d.D, true);
+    const tbe_stack dup = stack(a[10], "dup", t, d.E, d.F, d.D, true);
+    const tbe_stack ddown = stack(a[11], "ddown", t, d.E, d.D, d.F, true);
+    const Scratch ws = scratch(a[12]);
+    return lib.ffn_backward(&d, dys.p, dys.ld, xs.p, xs.ld, offsets, &gate, &up, &down, pre.p,
+                            pre.ld, dxs.p, dxs.ld, &dgate, &dup, &ddown, ws.p, ws.bytes,
+                            stream_of(a[13]));
+  });
+}
+
+// A list or tuple of `count` tensors.
+struct List {
+  PyObject** item;
+  List(PyObject* o, const char* name, Py_ssize_t count) {
+    if (!PyList_Check(o) && !PyTuple_Check(o)) refuse(name, "expected a list or tuple of tensors");
+    if (PySequence_Fast_GET_SIZE(o) != count) {
+      PyErr_Format(PyExc_TypeError, "%s: expected %zd tensors, got %zd", name, count,
+                   PySequence_Fast_GET_SIZE(o));
+      throw Refused{};
+    }
+    item = PySequence_Fast_ITEMS(o);
+  }
+};
+// A dense tensor of any shape with n elements.
+void* dense(PyObject* o, const char* name, at::ScalarType t, int64_t n) {
+  const at::Tensor& x = tensor(o, name, t);
+  if (x.numel() != n) {
+    PyErr_Format(PyExc_TypeError, "%s: expected %lld elements, got %lld", name, (long long)n,
+                 (long long)x.numel());
+    throw Refused{};
+  }
+  if (!x.is_contiguous()) refuse(name, "must be contiguous");
+  return x.data_ptr();
+}
+
+// adamw_step(desc, table, state, params, grads, step, lr, scale, copies, stream): `table`
+// is the state's array of tbe_adamw_tensor with the moments filled in, `state` one of
+// their buffers; the call fills in the rest.
+PyObject* adamw_step(PyObject*, Args args, Py_ssize_t n) {
+  return call<10>(args, n, [](Args a) {
+    const auto& d = desc<tbe_adamw_desc>(a[0]);
+    if (!PyTuple_Check(a[1]) || PyTuple_GET_SIZE(a[1]) != 2) refuse("state", "expected an AdamWState");
+    auto* t = static_cast<tbe_adamw_tensor*>(PyLong_AsVoidPtr(PyTuple_GET_ITEM(a[1], 0)));
+    const Py_ssize_t count = PyLong_AsSsize_t(PyTuple_GET_ITEM(a[1], 1));
+    if (PyErr_Occurred()) throw Refused{};
+    tensor(a[2], "state", d.bits == 32 ? at::kFloat : at::kFloat8_e4m3fn);
+    const List params(a[3], "params", count), grads(a[4], "grads", count);
+    const bool copy = d.cdtype >= 0;
+    if (copy == (a[8] == Py_None))
+      refuse("copies", copy ? "expected a list or tuple of tensors" : "the description has none");
+    PyObject** const copies = copy ? List(a[8], "copies", count).item : nullptr;
+    for (Py_ssize_t i = 0; i < count; ++i) {
+      t[i].p = dense(params.item[i], "params", type_of(d.pdtype), t[i].n);
+      t[i].g = dense(grads.item[i], "grads", type_of(d.gdtype), t[i].n);
+      t[i].c = copy ? dense(copies[i], "copies", type_of((tbe_dtype)d.cdtype), t[i].n) : nullptr;
+    }
+    auto* step = static_cast<const int64_t*>(vec(a[5], "step", at::kLong, 1));
+    auto* lr = static_cast<const float*>(vec(a[6], "lr", at::kFloat, 1));
+    auto* scale = a[7] == Py_None ? nullptr
+                                  : static_cast<const float*>(vec(a[7], "scale", at::kFloat, 1));
+    return lib.adamw_step(&d, t, count, step, lr, scale, stream_of(a[9]));
+  });
+}
+
 // bind(addresses): the entry points' addresses, in Entry's order.
 PyObject* bind(PyObject*, PyObject* addresses) {
   constexpr Py_ssize_t kEntries = sizeof(Entry) / sizeof(void*);
@@ -355,6 +511,11 @@ PyObject* bind(PyObject*, PyObject* addresses) {
   take(lib.distill_forward);
   take(lib.distill_backward);
   take(lib.distill_step);
+  take(lib.norm_forward);
+  take(lib.norm_backward);
+  take(lib.ffn_forward);
+  take(lib.ffn_backward);
+  take(lib.adamw_step);
   Py_RETURN_NONE;
 }
 
@@ -372,6 +533,11 @@ PyMethodDef methods[] = {
     TBE_METHOD(distill_forward),
     TBE_METHOD(distill_backward),
     TBE_METHOD(distill_step),
+    TBE_METHOD(norm_forward),
+    TBE_METHOD(norm_backward),
+    TBE_METHOD(ffn_forward),
+    TBE_METHOD(ffn_backward),
+    TBE_METHOD(adamw_step),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lmcall", nullptr, -1, methods,

@@ -8,6 +8,10 @@
  *            gradients of both
  *   distill  distillation loss of a student's logits against a teacher's top
  *            logits, and its gradient
+ *   norm     layer norm of rows, and its gradients
+ *   ffn      the experts' gated feed-forward products over rows sorted by
+ *            expert, and their gradients
+ *   adamw    one AdamW step over many tensors, moments in 32 or in 8 bits
  *
  * Conventions are those of tbe.h: the caller owns every buffer, nothing is
  * allocated, work is enqueued on `stream` (a hipStream_t, NULL = the null
@@ -171,6 +175,144 @@ tbe_status tbe_distill_backward(const tbe_distill_desc* desc, const void* x, int
 tbe_status tbe_distill_step(const tbe_distill_desc* desc, const void* x, int64_t ldx,
                             const void* ids, const void* t, const float* gl, float* loss,
                             void* gx, int64_t ldgx, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- layer norm -------------------------------------------------------------
+ *   mean[n] = mean over d of x[n, d]
+ *   rstd[n] = 1 / sqrt(mean over d of (x[n, d] - mean[n])^2 + eps)
+ *   xh[n, d] = (x[n, d] - mean[n]) * rstd[n]
+ *   y[n, d]  = xh[n, d] * w[d] + b[d]
+ * and with a[n, d] = dy[n, d] * w[d]
+ *   dx[n, d] = rstd[n] * (a - mean over d of a - xh * mean over d of a * xh)
+ *   dw[d] = sum over n of dy * xh          db[d] = sum over n of dy
+ * A NULL w stands for ones, a NULL b for zeros. 1 <= D <= 2^28, N < 2^31 - 1,
+ * eps finite and >= 0 (with eps 0 a row of equal values gives NaN). */
+typedef struct {
+    int64_t N;            /* rows, >= 0 */
+    int32_t D;            /* columns */
+    tbe_dtype dtype;      /* element type of x, y and their gradients */
+    tbe_dtype wdtype;     /* element type of w, b and their gradients */
+    float eps;
+} tbe_norm_desc;
+
+/* x: device [N, D]. w, b: device [D], dense, each may be NULL. y: device
+ * [N, D], overwritten. stats: device float32 [N, 2], overwritten: mean and
+ * rstd of each row, for the backward. */
+tbe_status tbe_norm_forward(const tbe_norm_desc* desc, const void* x, int64_t ldx, const void* w,
+                            const void* b, void* y, int64_t ldy, float* stats, void* stream);
+
+/* Bytes of the backward's workspace (0 on a bad description), as above. */
+size_t tbe_norm_workspace_bytes(const tbe_norm_desc* desc);
+
+/* dy: device [N, D]. dx: device [N, D], overwritten. dw, db: device [D],
+ * dense, overwritten (zeros when N = 0); each may be NULL, which leaves it
+ * out. Where the mean's rounding to float32 matters (|mean| far above the
+ * deviation) the call corrects it from x. */
+tbe_status tbe_norm_backward(const tbe_norm_desc* desc, const void* dy, int64_t lddy,
+                             const void* x, int64_t ldx, const void* w, const float* stats,
+                             void* dx, int64_t lddx, void* dw, void* db, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/* ---- experts' gated feed-forward ---------------------------------------------
+ * Row r of xs belongs to expert e when offsets[e] <= r < offsets[e + 1]
+ * (tbe_expert_plan's offsets, tbe_expert_dispatch's rows). With its matrices
+ *   g = xs[r, :] gate[e]^T      u = xs[r, :] up[e]^T       [F]
+ *   h = act(g) * u              ys[r, :] = h down[e]^T     [D]
+ * One expert and offsets 0, M make it a dense gated feed-forward block.
+ * Rows that belong to no expert are not read, and left as they are in every
+ * output. Offsets are read on the device; one below its predecessor or outside
+ * [0, M] is taken for the nearest that is neither.
+ * Products accumulate in float32. In 16-bit types pre, h and the gradients of
+ * g and u are rounded to the type between the products that use them.
+ * 1 <= E <= 1023, 1 <= D, F <= 65536, M * max(D, 2 F) <= 2^36,
+ * E * D * F <= 2^36, M < 2^31 - 1. */
+typedef enum { TBE_ACT_SILU = 0, TBE_ACT_GELU = 1 } tbe_act;   /* GELU by the error function */
+
+typedef struct {
+    int64_t M;            /* rows, >= 0 */
+    int32_t E;            /* experts */
+    int32_t D;            /* columns of a row */
+    int32_t F;            /* columns between the products */
+    tbe_dtype dtype;      /* element type of every matrix */
+    int32_t act;          /* tbe_act */
+} tbe_ffn_desc;
+
+/* E matrices: element (r, c) of matrix e is data[e * stride + r * ld + c].
+ * An input's ld and stride may be any values >= 0; an output's rows and
+ * matrices must not overlap (ld >= columns, stride >= rows * ld where E > 1). */
+typedef struct {
+    void* data;
+    int64_t ld;
+    int64_t stride;
+} tbe_stack;
+
+/* Bytes of the workspace of both calls (0 on a bad description), as above. */
+size_t tbe_ffn_workspace_bytes(const tbe_ffn_desc* desc);
+
+/* xs: device [M, D]. offsets: device int32 [E + 1]. gate, up: [E] of [F, D],
+ * down: [E] of [D, F], device, read only. pre: device [M, 2 F], overwritten
+ * with g and u beside each other, for the backward; may be NULL. ys: device
+ * [M, D], overwritten. */
+tbe_status tbe_ffn_forward(const tbe_ffn_desc* desc, const void* xs, int64_t ldxs,
+                           const int32_t* offsets, const tbe_stack* gate, const tbe_stack* up,
+                           const tbe_stack* down, void* pre, int64_t ldpre, void* ys,
+                           int64_t ldys, void* ws, size_t ws_bytes, void* stream);
+
+/* dys: device [M, D]; pre as the forward left it. dxs: device [M, D],
+ * overwritten. dgate, dup: [E] of [F, D], ddown: [E] of [D, F], device,
+ * overwritten (zeros for an expert without rows). */
+tbe_status tbe_ffn_backward(const tbe_ffn_desc* desc, const void* dys, int64_t lddys,
+                            const void* xs, int64_t ldxs, const int32_t* offsets,
+                            const tbe_stack* gate, const tbe_stack* up, const tbe_stack* down,
+                            const void* pre, int64_t ldpre, void* dxs, int64_t lddxs,
+                            const tbe_stack* dgate, const tbe_stack* dup, const tbe_stack* ddown,
+                            void* ws, size_t ws_bytes, void* stream);
+
+/* ---- AdamW ------------------------------------------------------------------
+ * With g the gradient times *scale, t = *step (counted from 1; less is taken
+ * for 1) and *lr, element by element over all tensors of the call:
+ *   m = beta1 m + (1 - beta1) g       v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay)
+ *       - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * in float32, p rounded once to its type. step, lr and scale are device memory
+ * and read by the kernels, so a captured step follows them.
+ * bits = 32: m and v are float32. bits = 8: each moment is an e4m3 number (4
+ * exponent and 3 mantissa bits, up to 448) times the float32 scale of its
+ * block of 256 elements, counted from the tensor's start; the scale is the
+ * block's largest magnitude / 448. m holds the moment, v the root of the
+ * second moment; a root above zero is held as at least the smallest number, so
+ * that no update is divided by eps alone. Blocks whose largest magnitude is
+ * below 2^-100 are held as zeros, a moment that is not finite as NaN (its
+ * block's others keep theirs). All buffers zero is the state before step 1. */
+typedef struct {
+    tbe_dtype pdtype;     /* element type of the parameters */
+    tbe_dtype gdtype;     /* of the gradients */
+    int32_t cdtype;       /* of the copies: TBE_F16 or TBE_BF16 with float32 parameters, -1: none */
+    int32_t bits;         /* 32 or 8 */
+    double beta1, beta2;  /* in [0, 1) */
+    double eps;           /* >= 0, finite */
+    double weight_decay;  /* >= 0, finite */
+} tbe_adamw_desc;
+
+/* One tensor of n elements, dense, any start (8-bit moments: a multiple of 8
+ * bytes). Nothing that is written may overlap; a parameter or a copy that
+ * overlaps another one is refused. */
+typedef struct {
+    void* p;              /* parameters, updated */
+    const void* g;        /* gradients */
+    void* m;              /* moments, updated */
+    void* v;
+    float* mscale;        /* [(n + 255) / 256], updated; bits = 8 only */
+    float* vscale;
+    void* c;              /* the new parameters rounded to cdtype, overwritten; cdtype >= 0 only */
+    int64_t n;            /* elements, >= 0 */
+} tbe_adamw_tensor;
+
+/* tensors: HOST array of `count`, read during the call. step: device int64.
+ * lr: device float32. scale: device float32, NULL for 1. count < 2^24,
+ * n < 2^40. */
+tbe_status tbe_adamw_step(const tbe_adamw_desc* desc, const tbe_adamw_tensor* tensors,
+                          int64_t count, const int64_t* step, const float* lr,
+                          const float* scale, void* stream);
 
 #ifdef __cplusplus
 }
