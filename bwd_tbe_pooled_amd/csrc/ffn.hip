@@ -79,9 +79,10 @@ __device__ __forceinline__ const T* matrix(const tbe_stack& m, int32_t e) {
   return static_cast<const T*>(m.data) + (int64_t)e * m.stride;
 }
 
-template <typename T, Product P, class S, bool VEC>
+template <typename T, Product P, class S, bool DIRECT>
 __global__ __launch_bounds__(S::NT) void ffn_kernel(Args g) {
   __shared__ __attribute__((aligned(16))) char lds[2 * S::AREA];
+  auto steps = [](int32_t k) { return (k + kStepBytes / (int)sizeof(T) - 1) / (kStepBytes / (int)sizeof(T)); };
   const int64_t tile = xcd_logical_block(g.tiles);
   if (tile < 0) return;
   const int wave = wave_index(), lane = lane_id();
@@ -108,11 +109,14 @@ __global__ __launch_bounds__(S::NT) void ffn_kernel(Args g) {
     const T* a = static_cast<const T*>(which == 2 ? g.dys : g.a) + (which == 1 ? g.half : 0);
     const T* b = static_cast<const T*>(which == 2 ? g.h : g.xs);
     const int64_t lda = which == 2 ? g.lddys : g.lda, ldb = which == 2 ? g.ldh : g.ldxs;
-    Operand<T, Across, S::BM, S::NT, VEC> oa;
-    Operand<T, Across, S::BN, S::NT, VEC> ob;
-    oa.start(rows - m0, lda, [&](int) { return a + (int64_t)s.first * lda + m0; });
-    ob.start(cols - n0, ldb, [&](int) { return b + (int64_t)s.first * ldb + n0; });
-    multiply<T, S>(acc, oa, ob, s.end - s.first, lds, [&](int j) { return (wn * S::NF + j) * 16; });
+    Operand<T, Across, S::BM, S::NT, DIRECT> oa;
+    Operand<T, Across, S::BN, S::NT, DIRECT> ob;
+    const int32_t K = s.end - s.first;
+    a += (int64_t)s.first * lda + m0;
+    b += (int64_t)s.first * ldb + n0;
+    oa.start(rows - m0, lda, K, [&](int) { return a; }, a);
+    ob.start(cols - n0, ldb, K, [&](int) { return b; }, b);
+    multiply<T, S, DIRECT>(acc, oa, ob, steps(K), 0, lds, [&](int j) { return (wn * S::NF + j) * 16; }, [] {});
     const tbe_stack& o = which == 0 ? g.o0 : which == 1 ? g.o1 : g.o2;
     T* out = static_cast<T*>(o.data) + (int64_t)s.e * o.stride;
 #pragma unroll
@@ -135,38 +139,42 @@ __global__ __launch_bounds__(S::NT) void ffn_kernel(Args g) {
     constexpr int BN = P == Up ? S::BN / 2 : S::BN;
     const int32_t n0 = s.place / s.tiles * BN;
     const int32_t N = P == Up || P == Dh ? g.F : g.D;
-    const T* a = static_cast<const T*>(g.a);
-    const int32_t last = s.end - 1;
-    Operand<T, Along, S::BM, S::NT, VEC> oa;
-    oa.start(S::BM, g.lda, [&](int r) { return a + (int64_t)min(m0 + r, last) * g.lda; });
+    const T* a = static_cast<const T*>(g.a) + (int64_t)m0 * g.lda;
+    const int32_t last = s.end - 1 - m0;
+    const int32_t K = P == Up || P == Dh ? g.D : g.F;
+    Operand<T, Along, S::BM, S::NT, DIRECT> oa;
+    oa.start(S::BM, g.lda, K, [&](int r) { return a + (int64_t)min(r, last) * g.lda; }, a);
+    Operand<T, P == Up || P == Down ? Along : Across, S::BN, S::NT, DIRECT, P == Up> ob;
+    const T* b0 = matrix<T>(g.b0, s.e);
     constexpr int HALF = S::NF / 2;
+    auto row_b = [&](int j) { return (wn * S::NF + j) * 16; };
     if constexpr (P == Up) {
       static_assert(S::NF % 2 == 0, "both products in one wave");
-      const T *b0 = matrix<T>(g.b0, s.e), *b1 = matrix<T>(g.b1, s.e);
-      Operand<T, Along, S::BN, S::NT, VEC> ob;
-      ob.start(S::BN, 0, [&](int r) {
-        const int64_t n = min(n0 + (r < BN ? r : r - BN), N - 1);
+      const T* b1 = matrix<T>(g.b1, s.e);
+      b0 += (int64_t)n0 * g.b0.ld;
+      b1 += (int64_t)n0 * g.b1.ld;
+      ob.start(S::BN, 0, K, [&](int r) {   // rows of up behind those of gate
+        const int64_t n = min(r < BN ? r : r - BN, N - 1 - n0);
         return r < BN ? b0 + n * g.b0.ld : b1 + n * g.b1.ld;
-      });
-      multiply<T, S>(acc, oa, ob, g.D, lds, [&](int j) {
+      }, b0, b1);
+      multiply<T, S, DIRECT>(acc, oa, ob, steps(K), 0, lds, [&](int j) {
         return j < HALF ? (wn * HALF + j) * 16 : BN + (wn * HALF + j - HALF) * 16;
-      });
+      }, [] {});
     } else if constexpr (P == Down) {
-      const T* b0 = matrix<T>(g.b0, s.e);
-      Operand<T, Along, S::BN, S::NT, VEC> ob;
-      ob.start(S::BN, 0, [&](int r) { return b0 + (int64_t)min(n0 + r, N - 1) * g.b0.ld; });
-      multiply<T, S>(acc, oa, ob, g.F, lds, [&](int j) { return (wn * S::NF + j) * 16; });
+      b0 += (int64_t)n0 * g.b0.ld;
+      ob.start(S::BN, 0, K, [&](int r) { return b0 + (int64_t)min(r, N - 1 - n0) * g.b0.ld; }, b0);
+      multiply<T, S, DIRECT>(acc, oa, ob, steps(K), 0, lds, row_b, [] {});
     } else {
-      const T* b0 = matrix<T>(g.b0, s.e);
-      Operand<T, Across, S::BN, S::NT, VEC> ob;
-      ob.start(N - n0, g.b0.ld, [&](int) { return b0 + n0; });
-      auto row_b = [&](int j) { return (wn * S::NF + j) * 16; };
-      multiply<T, S>(acc, oa, ob, P == Dh ? g.D : g.F, lds, row_b);
-      if constexpr (P == Dx) {
-        const T* b1 = matrix<T>(g.b1, s.e);
-        oa.start(S::BM, g.lda, [&](int r) { return a + g.half + (int64_t)min(m0 + r, last) * g.lda; });
-        ob.start(N - n0, g.b1.ld, [&](int) { return b1 + n0; });
-        multiply<T, S>(acc, oa, ob, g.F, lds, row_b);
+      b0 += n0;
+      ob.start(N - n0, g.b0.ld, K, [&](int) { return b0; }, b0);
+      if constexpr (P == Dh) {
+        multiply<T, S, DIRECT>(acc, oa, ob, steps(K), 0, lds, row_b, [] {});
+      } else {
+        multiply<T, S, DIRECT>(acc, oa, ob, steps(K), steps(K), lds, row_b, [&] {
+          const T *a1 = a + g.half, *b1 = matrix<T>(g.b1, s.e) + n0;
+          oa.start(S::BM, g.lda, K, [&](int r) { return a1 + (int64_t)min(r, last) * g.lda; }, a1);
+          ob.start(N - n0, g.b1.ld, K, [&](int) { return b1; }, b1);
+        });
       }
     }
 #pragma unroll
@@ -222,7 +230,7 @@ int64_t blocks_of(int64_t n, int64_t b) { return (n + b - 1) / b; }
 
 // Launches one product with tiles of shape S.
 template <typename T, Product P, class S>
-hipError_t launch(Args g, bool vec, hipStream_t s) {
+hipError_t launch(Args g, bool direct, hipStream_t s) {
   if constexpr (P == Dw) {
     g.tiles = (int64_t)g.E * (2 * blocks_of(g.F, S::BM) * blocks_of(g.D, S::BN) +
                               blocks_of(g.D, S::BM) * blocks_of(g.F, S::BN));
@@ -233,17 +241,18 @@ hipError_t launch(Args g, bool vec, hipStream_t s) {
     g.tiles = (g.M / S::BM + std::min(g.E, g.M)) * (int64_t)g.nt;
   }
   const unsigned grid = (unsigned)xcd_grid(g.tiles);
-  if (vec) ffn_kernel<T, P, S, true><<<grid, S::NT, 0, s>>>(g);
-  else ffn_kernel<T, P, S, false><<<grid, S::NT, 0, s>>>(g);
+  if (direct) ffn_kernel<T, P, S, true><<<grid, S::NT, 0, s>>>(g);
+  else if constexpr (S::NT == 256) ffn_kernel<T, P, S, false><<<grid, S::NT, 0, s>>>(g);
   return hipGetLastError();
 }
 
-// Whether all pieces of 16 bytes lie whole and aligned in their matrices.
+// Whether all pieces of 16 bytes lie whole and aligned in their matrices, and a tile's
+// rows within the 2 GiB that a direct load's offsets reach.
 struct Aligned {
   size_t size;
   bool ok = true;
   void rows(const void* p, int64_t ld) {
-    ok = ok && reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0;
+    ok = ok && reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0 && ld < (1 << 20);
   }
   void stack(const tbe_stack& m) {
     rows(m.data, m.ld);
@@ -252,6 +261,15 @@ struct Aligned {
 };
 
 using Middle = Shape<2, 2, 4, 4>;   // 128 x 128
+using Large = Shape<2, 4, 8, 4>;    // 256 x 256
+
+// Launches one product with the tiles that suit it.
+template <typename T, Product P>
+hipError_t launch_product(const Args& g, bool direct, hipStream_t s) {
+  if constexpr (sizeof(T) == 2)
+    if (direct && g.M / g.E >= 256) return launch<T, P, Large>(g, direct, s);
+  return launch<T, P, Middle>(g, direct, s);
+}
 
 }  // namespace
 
@@ -282,12 +300,12 @@ hipError_t launch_ffn_forward(const tbe_ffn_desc& d, const FfnForward& a, hipStr
     g.b0 = a.gate; g.b1 = a.up;
     g.c = a.ws + L.h; g.ldc = L.ld;
     g.c2 = a.pre; g.ldc2 = a.ldpre;
-    hipError_t e = launch<T, Up, Middle>(g, al.ok, s);
+    hipError_t e = launch_product<T, Up>(g, al.ok, s);
     if (e != hipSuccess) return e;
     g.a = a.ws + L.h; g.lda = L.ld;
     g.b0 = a.down;
     g.c = a.ys; g.ldc = a.ldys;
-    return launch<T, Down, Middle>(g, al.ok, s);
+    return launch_product<T, Down>(g, al.ok, s);
   });
 }
 
@@ -311,12 +329,12 @@ hipError_t launch_ffn_backward(const tbe_ffn_desc& d, const FfnBackward& a, hipS
       g.pre = a.pre; g.ldpre = a.ldpre;
       g.c = a.ws + L.h; g.ldc = L.ld;
       g.c2 = a.ws + L.dgu; g.ldc2 = 2 * L.ld;
-      hipError_t e = launch<T, Dh, Middle>(g, al.ok, s);
+      hipError_t e = launch_product<T, Dh>(g, al.ok, s);
       if (e != hipSuccess) return e;
       g.a = a.ws + L.dgu; g.lda = 2 * L.ld;
       g.b0 = a.gate; g.b1 = a.up;
       g.c = a.dxs; g.ldc = a.lddxs;
-      e = launch<T, Dx, Middle>(g, al.ok, s);
+      e = launch_product<T, Dx>(g, al.ok, s);
       if (e != hipSuccess) return e;
     }
     g.a = a.ws + L.dgu; g.lda = 2 * L.ld;
@@ -324,7 +342,7 @@ hipError_t launch_ffn_backward(const tbe_ffn_desc& d, const FfnBackward& a, hipS
     g.xs = a.xs; g.ldxs = a.ldxs;
     g.h = a.ws + L.h; g.ldh = L.ld;
     g.o0 = a.dgate; g.o1 = a.dup; g.o2 = a.ddown;
-    return launch<T, Dw, Middle>(g, al.ok, s);
+    return launch_product<T, Dw>(g, al.ok, s);
   });
 }
 

@@ -61,55 +61,113 @@ __device__ __forceinline__ uint32_t across_at(int k, int b) {
   return (uint32_t)(k * BYTES + ((((b >> 5) ^ f) & (BYTES / 32 - 1)) << 5) + (b & 31));
 }
 
-// One operand's pieces of a step, from memory through registers to LDS. ROWS: of
-// the tile, NT: threads; VEC: pieces lie in the matrix whole or not at all.
-template <typename T, Layout L, int ROWS, int NT, bool VEC>
+// One operand's pieces of a step, from memory to LDS. ROWS: of the tile, NT:
+// threads. DIRECT: every piece lies in its matrix whole and aligned, and goes to
+// LDS without a register in between; otherwise it passes through registers, where
+// elements outside become zeros one by one. SPLIT: the second half of the rows is
+// another matrix's.
+template <typename T, Layout L, int ROWS, int NT, bool DIRECT, bool SPLIT = false>
 struct Operand {
   static constexpr int VE = 16 / (int)sizeof(T);
   static constexpr int BK = kStepBytes / (int)sizeof(T);
   static constexpr int BYTES = ROWS * (int)sizeof(T);        // of a row of Across
+  static constexpr int PER = BYTES / 16;                     // its pieces
   static constexpr int PIECES = ROWS * (kStepBytes / 16) / NT;
+  static constexpr int READS = L == Along ? 1 : sizeof(T) == 2 ? 2 : 4;   // of LDS, for a fragment
   static_assert(PIECES * NT * 16 == ROWS * kStepBytes, "whole pieces per thread");
-  const T* p[PIECES];
+  int32_t limit;     // Across: columns behind the tile's start
+  int32_t left;      // elements of k not loaded yet
   int64_t step;      // elements from one step to the next
-  int32_t limit;     // Across: columns behind p's tile start
-  uint4 r[PIECES];
+  // through registers
+  const T* p[DIRECT ? 1 : PIECES];
+  uint4 r[DIRECT ? 1 : PIECES];
+  // direct
+  const T* base[1 + SPLIT];
+  uint32_t off[DIRECT ? PIECES : 1];
+
+  // Piece i of this thread: row (of the tile, or of k) and column in pieces. Direct
+  // pieces are written in the order of threads, so it is the source that is permuted.
+  static __device__ __forceinline__ void place(int i, int& row, int& col) {
+    const int at = (int)threadIdx.x + i * NT;
+    if constexpr (L == Along) {
+      row = at / 8;
+      col = DIRECT ? (at % 8) ^ (row & 7) : at % 8;
+    } else {
+      row = at / PER;
+      col = at % PER;
+      if (DIRECT) col = (int)(across_at<T, BYTES>(row, col * 16) % BYTES) / 16;
+    }
+  }
 
   // row(i): address of row i of the tile. Along, rows from `rows` on repeat the
   // last one (their products are not stored); Across, the tile has `rows` columns.
+  // first: an address at or before every piece's; second: of the second matrix's.
   template <typename Row>
-  __device__ __forceinline__ void start(int32_t rows, int64_t ld, Row row) {
+  __device__ __forceinline__ void start(int32_t rows, int64_t ld, int32_t K, Row row, const T* first,
+                                        const T* second = nullptr) {
     limit = rows;
+    left = K;
+    base[0] = first;
+    if constexpr (SPLIT) base[1] = second;
+    step = L == Along ? BK : BK * ld;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-      const int at = (int)threadIdx.x + i * NT;
-      if constexpr (L == Along) {
-        const int q = at / 8;
-        p[i] = row(q) + (at % 8) * VE;
+      int q, c;
+      place(i, q, c);
+      const T* from = L == Along ? row(q) + c * VE : row(0) + (int64_t)q * ld + c * VE;
+      if constexpr (DIRECT) {
+        off[i] = (uint32_t)((from - (SPLIT && i >= PIECES / 2 ? second : first)) * (int64_t)sizeof(T));
+        if (L == Across && c * VE >= rows) off[i] = kOutside;
       } else {
-        constexpr int PER = BYTES / 16;
-        p[i] = row(0) + (int64_t)(at / PER) * ld + (at % PER) * VE;
+        p[i] = from;
       }
     }
-    step = L == Along ? BK : BK * ld;
   }
 
-  // Loads the pieces of the step at k of K; zeros outside.
-  __device__ __forceinline__ void load(int32_t k, int32_t K) {
+  // Direct: the next step's pieces on their way to `lds`, zeros outside. No register
+  // is written, so the compiler needs no part in waiting for them: multiply does.
+  static constexpr uint32_t kOutside = 0x80000000u;
+  __device__ __forceinline__ void fetch(uint32_t lds) {
+    typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+    i32x4 rsrc[1 + SPLIT];
+#pragma unroll
+    for (int j = 0; j <= SPLIT; ++j) {
+      const uint64_t at = reinterpret_cast<uint64_t>(base[j]);
+      rsrc[j] = {__builtin_amdgcn_readfirstlane((int)at), __builtin_amdgcn_readfirstlane((int)(at >> 32) & 0xffff),
+                 (int)kOutside, 0x00020000};
+      base[j] += step;
+    }
+    const bool whole = left >= BK;
+    const uint32_t to = __builtin_amdgcn_readfirstlane(lds + wave_index() * (kWave * 16));
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-      const int at = (int)threadIdx.x + i * NT;
-      int n;   // elements of the piece that exist
-      if constexpr (L == Along) {
-        n = K - k - (at % 8) * VE;
-      } else {
-        constexpr int PER = BYTES / 16;
-        n = k + at / PER < K ? limit - (at % PER) * VE : 0;
+      uint32_t from = off[i];
+      if (!whole) {
+        int q, c;
+        place(i, q, c);
+        if ((L == Along ? c * VE : q) >= left) from = kOutside;
       }
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"   // m0 is reserved: the compiler keeps nothing in it
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                   :: "s"(to + i * (NT * 16)), "v"(from), "s"(rsrc[SPLIT && i >= PIECES / 2 ? 1 : 0]) : "m0");
+#pragma clang diagnostic pop
+    }
+    left -= BK;
+  }
+
+  // Through registers: loads the next step's pieces; zeros outside.
+  __device__ __forceinline__ void load() {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      int q, c;
+      place(i, q, c);
+      // elements of the piece that exist
+      const int n = L == Along ? left - c * VE : q < left ? limit - c * VE : 0;
       r[i] = make_uint4(0, 0, 0, 0);
       if (n >= VE) {
         r[i] = __builtin_bit_cast(uint4, load_pack<T, VE>(p[i]));
-      } else if (!VEC && n > 0) {
+      } else if (n > 0) {
         T e[VE];
 #pragma unroll
         for (int j = 0; j < VE; ++j) e[j] = j < n ? p[i][j] : T{};
@@ -117,20 +175,14 @@ struct Operand {
       }
       p[i] += step;
     }
+    left -= BK;
   }
-
   __device__ __forceinline__ void store(char* lds) const {
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-      const int at = (int)threadIdx.x + i * NT;
-      uint32_t to;
-      if constexpr (L == Along) {
-        to = along_at(at / 8, at % 8);
-      } else {
-        constexpr int PER = BYTES / 16;
-        to = across_at<T, BYTES>(at / PER, (at % PER) * 16);
-      }
-      *reinterpret_cast<uint4*>(lds + to) = r[i];
+      int q, c;
+      place(i, q, c);
+      *reinterpret_cast<uint4*>(lds + (L == Along ? along_at(q, c) : across_at<T, BYTES>(q, c * 16))) = r[i];
     }
   }
 
@@ -169,45 +221,111 @@ struct Shape {
   static constexpr int AREA = (BM + BN) * kStepBytes;   // of LDS for one step
 };
 
-// acc += the product over K. `row_b(nf)`: first of the 16 rows of B's tile that
+// A wave's fragments of half a step.
+template <class S>
+struct Frags {
+  uint4 a[S::MF], b[S::NF];
+  template <class A, class B, typename RowB>
+  __device__ __forceinline__ void read(const char* lds, int s, RowB row_b) {
+    const int wm = wave_index() / S::WN;
+#pragma unroll
+    for (int j = 0; j < S::NF; ++j) b[j] = B::frag(lds + S::BM * kStepBytes, row_b(j), s);
+#pragma unroll
+    for (int i = 0; i < S::MF; ++i) a[i] = A::frag(lds, (wm * S::MF + i) * 16, s);
+  }
+  template <typename T>
+  __device__ __forceinline__ void mul(f32x4 (&acc)[S::MF][S::NF]) const {
+#pragma unroll
+    for (int i = 0; i < S::MF; ++i)
+#pragma unroll
+      for (int j = 0; j < S::NF; ++j) acc[i][j] = Mma<T>::mul(b[j], a[i], acc[i][j]);
+  }
+};
+
+// Asks the scheduler for READS reads of LDS spread over PRODUCTS products.
+template <int READS, int PRODUCTS>
+__device__ __forceinline__ void interleave() {
+  constexpr int EACH = PRODUCTS / READS;
+#pragma unroll
+  for (int i = 0; i < READS; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, EACH, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, PRODUCTS - READS * EACH, 0);
+}
+
+// acc += the product over the steps of k: `steps` of the operands as they are,
+// then `more` after turn(). `row_b(nf)`: first of the 16 rows of B's tile that
 // fragment nf of this wave takes.
-template <typename T, class S, class A, class B, typename RowB>
-__device__ __forceinline__ void multiply(f32x4 (&acc)[S::MF][S::NF], A& a, B& b, int32_t K,
-                                         char* lds, RowB row_b) {
-  constexpr int BK = kStepBytes / (int)sizeof(T);
-  const int steps = (K + BK - 1) / BK;
-  if (steps == 0) return;
-  const int wm = wave_index() / S::WN;
-  a.load(0, K);
-  b.load(0, K);
-  __syncthreads();   // the areas' last readers are done
-  a.store(lds);
-  b.store(lds + S::BM * kStepBytes);
-  __syncthreads();
-  for (int i = 0; i < steps; ++i) {
-    const char* now = lds + (i & 1) * S::AREA;
-    if (i + 1 < steps) {
-      a.load((i + 1) * BK, K);
-      b.load((i + 1) * BK, K);
+//
+// Direct: behind the barrier of step i its data are in one area of LDS and no wave
+// reads the other any more. A wave then multiplies the second half of step i - 1,
+// which it has in registers, while it reads the first half of step i, and so on:
+// reads of LDS and products always have each other to run beside.
+template <typename T, class S, bool DIRECT, class A, class B, typename RowB, typename Turn>
+__device__ __forceinline__ void multiply(f32x4 (&acc)[S::MF][S::NF], A& a, B& b, int steps, int more,
+                                         char* lds, RowB row_b, Turn turn) {
+  const int all = steps + more;
+  if (all == 0) return;
+  if constexpr (DIRECT) {
+    constexpr int kReads = S::MF * A::READS + S::NF * B::READS;
+    constexpr int kProducts = S::MF * S::NF * (sizeof(T) == 4 ? 4 : 1);
+    typedef __attribute__((address_space(3))) char* lds_ptr;
+    const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr)lds;
+    auto arrived = [&]() {
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" :: "s"(base) : "memory");
+    };
+    auto fetch = [&](int i) {
+      if (i == steps) turn();
+      const uint32_t to = base + (i & 1) * S::AREA;
+      a.fetch(to);
+      b.fetch(to + S::BM * kStepBytes);
+    };
+    Frags<S> even, odd;
+    fetch(0);
+    arrived();
+    if (all > 1) fetch(1);
+    even.template read<A, B>(lds, 0, row_b);
+    odd.template read<A, B>(lds, 1, row_b);
+    even.template mul<T>(acc);
+    for (int i = 1; i < all; ++i) {
+      arrived();
+      if (i + 1 < all) fetch(i + 1);
+      const char* now = lds + (i & 1) * S::AREA;
+      even.template read<A, B>(now, 0, row_b);
+      odd.template mul<T>(acc);
+      interleave<kReads, kProducts>();
+      odd.template read<A, B>(now, 1, row_b);
+      even.template mul<T>(acc);
+      interleave<kReads, kProducts>();
     }
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      uint4 fa[S::MF], fb[S::NF];
-#pragma unroll
-      for (int i = 0; i < S::MF; ++i) fa[i] = A::frag(now, (wm * S::MF + i) * 16, s);
-#pragma unroll
-      for (int j = 0; j < S::NF; ++j) fb[j] = B::frag(now + S::BM * kStepBytes, row_b(j), s);
-#pragma unroll
-      for (int i = 0; i < S::MF; ++i)
-#pragma unroll
-        for (int j = 0; j < S::NF; ++j) acc[i][j] = Mma<T>::mul(fb[j], fa[i], acc[i][j]);
-    }
-    if (i + 1 < steps) {
-      char* next = lds + (~i & 1) * S::AREA;
-      a.store(next);
-      b.store(next + S::BM * kStepBytes);
-    }
+    odd.template mul<T>(acc);
+  } else {
+    auto load = [&](int i) {
+      if (i == steps) turn();
+      a.load();
+      b.load();
+    };
+    load(0);
+    a.store(lds);
+    b.store(lds + S::BM * kStepBytes);
     __syncthreads();
+    for (int i = 0; i < all; ++i) {
+      const char* now = lds + (i & 1) * S::AREA;
+      if (i + 1 < all) load(i + 1);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        Frags<S> f;
+        f.template read<A, B>(now, s, row_b);
+        f.template mul<T>(acc);
+      }
+      if (i + 1 < all) {
+        char* next = lds + (~i & 1) * S::AREA;
+        a.store(next);
+        b.store(next + S::BM * kStepBytes);
+      }
+      __syncthreads();
+    }
   }
 }
 
