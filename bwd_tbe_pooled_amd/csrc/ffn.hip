@@ -53,25 +53,34 @@ __device__ __forceinline__ void activate(int32_t act, float g, float& a, float& 
   }
 }
 
-// Up to four neighbouring elements of a row.
+// Up to eight neighbouring elements of a row.
 template <typename T>
-__device__ __forceinline__ void store4(T* p, int32_t n, const float (&f)[4]) {
-  if (n >= 4) {
-    store_pack<T, 4>(p, narrow<T, 4>(f));
+__device__ __forceinline__ void store8(T* p, int32_t n, const float (&f)[8]) {
+  if (n >= 8) {
+    store_pack<T, 8>(p, narrow<T, 8>(f));
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 8; ++j)
       if (j < n) p[j] = round_to<T>(f[j]);
   }
 }
 template <typename T>
-__device__ __forceinline__ void load4(const T* p, int32_t n, float (&f)[4]) {
-  if (n >= 4) {
-    widen<T, 4>(load_pack<T, 4>(p), f);
-  } else {
+__device__ __forceinline__ typename Pack<T, 8>::raw load8(const T* p, int32_t n) {
+  typename Pack<T, 8>::raw r{};
+  if (n >= 8) {
+    r = load_pack<T, 8>(p);
+  } else if (n > 0) {
+    T e[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = j < n ? to_float(p[j]) : 0.f;
+    for (int j = 0; j < 8; ++j) e[j] = j < n ? p[j] : T{};
+    r = __builtin_bit_cast(typename Pack<T, 8>::raw, e);
   }
+  return r;
+}
+
+__device__ __forceinline__ void eight(const f32x4& a, const f32x4& b, float (&f)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = a[j], f[j + 4] = b[j];
 }
 
 template <typename T>
@@ -124,20 +133,26 @@ __global__ __launch_bounds__(S::NT) void ffn_kernel(Args g) {
       const int32_t m = m0 + (wm * S::MF + i) * 16 + lane % 16;
       if (m >= rows) continue;
 #pragma unroll
-      for (int j = 0; j < S::NF; ++j) {
-        const int32_t n = n0 + (wn * S::NF + j) * 16 + lane / 16 * 4;
-        const float f[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-        store4<T>(out + (int64_t)m * o.ld + n, cols - n, f);
+      for (int j = 0; j < S::NF; j += 2) {
+        const int32_t n = n0 + (wn * S::NF + j) * 16 + lane / 16 * 8;
+        float f[8];
+        eight(acc[i][j], acc[i][j + 1], f);
+        if (n < cols) store8<T>(out + (int64_t)m * o.ld + n, cols - n, f);
       }
     }
     return;
   } else {
     Span s;
     if (!find_block<S::BM>(g.offsets, g.E, g.M, g.nt, (int32_t)tile, s)) return;
-    const int32_t m0 = s.first + s.place % s.tiles * S::BM;
+    // an expert's tiles in groups of 8 blocks of rows, in a group the rows first: the
+    // 32 tiles that an XCD works on share rows and matrices in its L2
+    constexpr int GROUP = 8;
+    const int32_t group = s.place / (GROUP * g.nt) * GROUP;
+    const int32_t high = min(GROUP, s.tiles - group), in = s.place - group * g.nt;
+    const int32_t m0 = s.first + (group + in % high) * S::BM;
     // columns of a tile: of Up's two products half each
     constexpr int BN = P == Up ? S::BN / 2 : S::BN;
-    const int32_t n0 = s.place / s.tiles * BN;
+    const int32_t n0 = in / high * BN;
     const int32_t N = P == Up || P == Dh ? g.F : g.D;
     const T* a = static_cast<const T*>(g.a) + (int64_t)m0 * g.lda;
     const int32_t last = s.end - 1 - m0;
@@ -154,7 +169,7 @@ __global__ __launch_bounds__(S::NT) void ffn_kernel(Args g) {
       b0 += (int64_t)n0 * g.b0.ld;
       b1 += (int64_t)n0 * g.b1.ld;
       ob.start(S::BN, 0, K, [&](int r) {   // rows of up behind those of gate
-        const int64_t n = min(r < BN ? r : r - BN, N - 1 - n0);
+        const int64_t n = min(column_of(r < BN ? r : r - BN), N - 1 - n0);
         return r < BN ? b0 + n * g.b0.ld : b1 + n * g.b1.ld;
       }, b0, b1);
       multiply<T, S, DIRECT>(acc, oa, ob, steps(K), 0, lds, [&](int j) {
@@ -162,7 +177,7 @@ __global__ __launch_bounds__(S::NT) void ffn_kernel(Args g) {
       }, [] {});
     } else if constexpr (P == Down) {
       b0 += (int64_t)n0 * g.b0.ld;
-      ob.start(S::BN, 0, K, [&](int r) { return b0 + (int64_t)min(r, N - 1 - n0) * g.b0.ld; }, b0);
+      ob.start(S::BN, 0, K, [&](int r) { return b0 + (int64_t)min(column_of(r), N - 1 - n0) * g.b0.ld; }, b0);
       multiply<T, S, DIRECT>(acc, oa, ob, steps(K), 0, lds, row_b, [] {});
     } else {
       b0 += n0;
@@ -177,50 +192,71 @@ __global__ __launch_bounds__(S::NT) void ffn_kernel(Args g) {
         });
       }
     }
+    // eight columns of a row at a time; Dh's rows of `pre` are loaded two ahead of
+    // the stores, which may go to the same memory for all the compiler knows
+    constexpr int COLS = P == Up ? HALF : S::NF;
+    constexpr int AHEAD = P == Dh ? 2 : 1;
+    static_assert(S::MF % AHEAD == 0 && COLS % 2 == 0, "whole groups");
+    const int32_t nw = n0 + wn * COLS * 16 + lane / 16 * 8;
 #pragma unroll
-    for (int i = 0; i < S::MF; ++i) {
-      const int32_t m = m0 + (wm * S::MF + i) * 16 + lane % 16;
-      if (m >= s.end) continue;
-      T* c = static_cast<T*>(g.c) + (int64_t)m * g.ldc;
-      T* c2 = static_cast<T*>(g.c2) + (int64_t)m * g.ldc2;
+    for (int i0 = 0; i0 < S::MF; i0 += AHEAD) {
+      [[maybe_unused]] typename Pack<T, 8>::raw pu[AHEAD][COLS / 2], pv[AHEAD][COLS / 2];
+      if constexpr (P == Dh) {
 #pragma unroll
-      for (int j = 0; j < (P == Up ? HALF : S::NF); ++j) {
-        const int32_t n = n0 + (wn * (P == Up ? HALF : S::NF) + j) * 16 + lane / 16 * 4;
-        if (n >= N) continue;
-        float f[4], u[4], v[4];
-        if constexpr (P == Up) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float da;
-            u[q] = acc[i][j][q];
-            v[q] = acc[i][j + HALF][q];
-            activate<T>(g.act, u[q], f[q], da);
-            f[q] *= v[q];
-          }
-          if (g.c2) {
-            store4<T>(c2 + n, N - n, u);
-            store4<T>(c2 + N + n, N - n, v);
-          }
-        } else if constexpr (P == Dh) {
+        for (int i = 0; i < AHEAD; ++i) {
+          const int32_t m = m0 + (wm * S::MF + i0 + i) * 16 + lane % 16;
           const T* pre = static_cast<const T*>(g.pre) + (int64_t)m * g.ldpre;
-          load4<T>(pre + n, N - n, u);
-          load4<T>(pre + N + n, N - n, v);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float dh = acc[i][j][q];
-            float x, da;
-            activate<T>(g.act, u[q], x, da);
-            f[q] = x * v[q];
-            u[q] = dh * v[q] * da;
-            v[q] = dh * x;
+          for (int j = 0; j < COLS; j += 2) {
+            const int32_t n = nw + j * 16;
+            pu[i][j / 2] = load8<T>(pre + n, m < s.end ? N - n : 0);
+            pv[i][j / 2] = load8<T>(pre + N + n, m < s.end ? N - n : 0);
           }
-          store4<T>(c2 + n, N - n, u);
-          store4<T>(c2 + g.half + n, N - n, v);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) f[q] = acc[i][j][q];
         }
-        store4<T>(c + n, N - n, f);
+      }
+#pragma unroll
+      for (int i = i0; i < i0 + AHEAD; ++i) {
+        const int32_t m = m0 + (wm * S::MF + i) * 16 + lane % 16;
+        if (m >= s.end) continue;
+        T* c = static_cast<T*>(g.c) + (int64_t)m * g.ldc;
+        T* c2 = static_cast<T*>(g.c2) + (int64_t)m * g.ldc2;
+#pragma unroll
+        for (int j = 0; j < COLS; j += 2) {
+          const int32_t n = nw + j * 16;
+          if (n >= N) continue;
+          float f[8];
+          eight(acc[i][j], acc[i][j + 1], f);
+          if constexpr (P == Up) {
+            float u[8];
+            eight(acc[i][j + HALF], acc[i][j + HALF + 1], u);
+            if (g.c2) {
+              store8<T>(c2 + n, N - n, f);
+              store8<T>(c2 + N + n, N - n, u);
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              float a, da;
+              activate<T>(g.act, f[q], a, da);
+              f[q] = a * u[q];
+            }
+          } else if constexpr (P == Dh) {
+            float u[8], v[8];
+            widen<T, 8>(pu[i - i0][j / 2], u);
+            widen<T, 8>(pv[i - i0][j / 2], v);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float dh = f[q];
+              float x, da;
+              activate<T>(g.act, u[q], x, da);
+              f[q] = x * v[q];
+              u[q] = dh * v[q] * da;
+              v[q] = dh * x;
+            }
+            store8<T>(c2 + n, N - n, u);
+            store8<T>(c2 + g.half + n, N - n, v);
+          }
+          store8<T>(c + n, N - n, f);
+        }
       }
     }
   }

@@ -9,7 +9,8 @@
 //
 // In LDS a 16-byte piece stands at a place permuted by its row, so that the
 // lanes of one read meet different banks. The wave multiplies B by A: a lane
-// then holds four neighbouring columns of one row of C.
+// then holds four columns of one row of C from each fragment, and as two
+// fragments take the fours of 32 columns in turn, eight neighbouring ones.
 #pragma once
 
 #include "lm.h"
@@ -50,15 +51,20 @@ enum Layout { Along, Across };
 
 // Byte offset of a piece in LDS. Along: row r, piece c of 8.
 __device__ __forceinline__ uint32_t along_at(int r, int c) {
-  return (uint32_t)(r * kStepBytes + ((c ^ (r & 7)) << 4));
+  return (uint32_t)(r * kStepBytes + ((c ^ ((r >> 1) & 7)) << 4));
 }
-// Across: row k, byte b of BYTES; 32-byte units are permuted: by k mod 4 and k / 8
-// for 16 bits, whose transposing reads take four rows and two rows 8 apart at a
-// time; in pairs by k / 4 for float32, where the four rows of one read are 4 apart.
+// The column that row r of B's tile holds: of 32, rows 0-15 take the first four of
+// each eight, rows 16-31 the others.
+__device__ __forceinline__ int column_of(int r) {
+  return (r & ~31) | ((r & 12) << 1) | ((r & 16) >> 2) | (r & 3);
+}
+// Across: row k, byte b of BYTES; 64-byte units are permuted: by k mod 4 for 16
+// bits, whose transposing reads take four rows at a time; by k / 4 for float32,
+// where the four rows of one read are 4 apart.
 template <typename T, int BYTES>
 __device__ __forceinline__ uint32_t across_at(int k, int b) {
-  const int f = sizeof(T) == 2 ? (k & 3) | ((k >> 1) & 4) : ((k >> 2) & 3) << 1;
-  return (uint32_t)(k * BYTES + ((((b >> 5) ^ f) & (BYTES / 32 - 1)) << 5) + (b & 31));
+  const int f = sizeof(T) == 2 ? k & 3 : (k >> 2) & 3;
+  return (uint32_t)(k * BYTES + ((((b >> 6) ^ f) & (BYTES / 64 - 1)) << 6) + (b & 63));
 }
 
 // One operand's pieces of a step, from memory to LDS. ROWS: of the tile, NT:
@@ -91,7 +97,7 @@ struct Operand {
     const int at = (int)threadIdx.x + i * NT;
     if constexpr (L == Along) {
       row = at / 8;
-      col = DIRECT ? (at % 8) ^ (row & 7) : at % 8;
+      col = DIRECT ? (at % 8) ^ ((row >> 1) & 7) : at % 8;
     } else {
       row = at / PER;
       col = at % PER;
@@ -186,8 +192,10 @@ struct Operand {
     }
   }
 
-  // A lane's part of 16 rows of the tile from `row`: row + lane % 16, and of half
-  // step s (64 bytes of k) the quarter lane / 16.
+  // A lane's part of 16 rows of the tile from `row`: row + lane % 16 (column_of it
+  // where the tile is Across and PERMUTE), and of half step s (64 bytes of k) the
+  // quarter lane / 16.
+  template <bool PERMUTE>
   static __device__ __forceinline__ uint4 frag(const char* lds, int row, int s) {
     const int lane = lane_id();
     if constexpr (L == Along) {
@@ -197,17 +205,18 @@ struct Operand {
       typedef short s16x4 __attribute__((ext_vector_type(4)));
       typedef __attribute__((address_space(3))) s16x4* lds_ptr;
       const int k = s * 32 + lane / 16 * 8 + lane % 16 / 4;
-      const int b = (row + lane % 4 * 4) * 2;
+      const int b = (PERMUTE ? (row & ~31) + lane % 4 * 8 + (row & 16) / 4 : row + lane % 4 * 4) * 2;
       union { s16x4 h[2]; uint4 u; } v;
       v.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lds + across_at<T, BYTES>(k, b)));
       v.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lds + across_at<T, BYTES>(k + 4, b)));
       return v.u;
     } else {
       uint32_t v[4];
+      const int col = PERMUTE ? column_of(row + lane % 16) : row + lane % 16;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         v[j] = *reinterpret_cast<const uint32_t*>(
-            lds + across_at<T, BYTES>(s * 16 + lane / 16 * 4 + j, (row + lane % 16) * 4));
+            lds + across_at<T, BYTES>(s * 16 + lane / 16 * 4 + j, col * 4));
       return make_uint4(v[0], v[1], v[2], v[3]);
     }
   }
@@ -229,9 +238,9 @@ struct Frags {
   __device__ __forceinline__ void read(const char* lds, int s, RowB row_b) {
     const int wm = wave_index() / S::WN;
 #pragma unroll
-    for (int j = 0; j < S::NF; ++j) b[j] = B::frag(lds + S::BM * kStepBytes, row_b(j), s);
+    for (int j = 0; j < S::NF; ++j) b[j] = B::template frag<true>(lds + S::BM * kStepBytes, row_b(j), s);
 #pragma unroll
-    for (int i = 0; i < S::MF; ++i) a[i] = A::frag(lds, (wm * S::MF + i) * 16, s);
+    for (int i = 0; i < S::MF; ++i) a[i] = A::template frag<false>(lds, (wm * S::MF + i) * 16, s);
   }
   template <typename T>
   __device__ __forceinline__ void mul(f32x4 (&acc)[S::MF][S::NF]) const {
