@@ -78,169 +78,186 @@ __device__ __forceinline__ typename Pack<T, 8>::raw load8(const T* p, int32_t n)
   return r;
 }
 
-__device__ __forceinline__ void eight(const f32x4& a, const f32x4& b, float (&f)[8]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) f[j] = a[j], f[j + 4] = b[j];
-}
-
 template <typename T>
 __device__ __forceinline__ const T* matrix(const tbe_stack& m, int32_t e) {
   return static_cast<const T*>(m.data) + (int64_t)e * m.stride;
 }
 
-template <typename T, Product P, class S, bool DIRECT>
-__global__ __launch_bounds__(S::NT) void ffn_kernel(Args g) {
-  __shared__ __attribute__((aligned(16))) char lds[2 * S::AREA];
-  auto steps = [](int32_t k) { return (k + kStepBytes / (int)sizeof(T) - 1) / (kStepBytes / (int)sizeof(T)); };
-  const int64_t tile = xcd_logical_block(g.tiles);
-  if (tile < 0) return;
-  const int wave = wave_index(), lane = lane_id();
-  const int wm = wave / S::WN, wn = wave % S::WN;
-  f32x4 acc[S::MF][S::NF];
-#pragma unroll
-  for (int i = 0; i < S::MF; ++i)
-#pragma unroll
-    for (int j = 0; j < S::NF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+// Where a tile lies.
+struct Tile {
+  int32_t e;
+  int32_t m0, n0;          // first row (Dw: of the matrix) and column
+  int32_t rows, cols;      // behind the last
+  int32_t K;
+  int32_t first;           // Dw: the expert's first row
+  int32_t which;           // Dw: gate's, up's or down's gradient
+};
 
-  if constexpr (P == Dw) {
-    // tiles of one expert: gate's, up's, down's
-    const int32_t ft = (g.F + S::BM - 1) / S::BM, dt = (g.D + S::BN - 1) / S::BN;
-    const int32_t dt2 = (g.D + S::BM - 1) / S::BM, ft2 = (g.F + S::BN - 1) / S::BN;
-    const int32_t each = ft * dt, per = 2 * each + dt2 * ft2;
-    Span s;
-    expert_rows(g.offsets, (int32_t)(tile / per), g.M, s);
-    const int32_t at = (int32_t)(tile % per);
-    const int which = at < each ? 0 : at < 2 * each ? 1 : 2;
-    const int32_t in = at - which * each;
-    const int32_t across = which == 2 ? ft2 : dt;
-    const int32_t m0 = in / across * S::BM, n0 = in % across * S::BN;
-    const int32_t rows = which == 2 ? g.D : g.F, cols = which == 2 ? g.F : g.D;
-    const T* a = static_cast<const T*>(which == 2 ? g.dys : g.a) + (which == 1 ? g.half : 0);
-    const T* b = static_cast<const T*>(which == 2 ? g.h : g.xs);
-    const int64_t lda = which == 2 ? g.lddys : g.lda, ldb = which == 2 ? g.ldh : g.ldxs;
-    Operand<T, Across, S::BM, S::NT, DIRECT> oa;
-    Operand<T, Across, S::BN, S::NT, DIRECT> ob;
-    const int32_t K = s.end - s.first;
-    a += (int64_t)s.first * lda + m0;
-    b += (int64_t)s.first * ldb + n0;
-    oa.start(rows - m0, lda, K, [&](int) { return a; }, a);
-    ob.start(cols - n0, ldb, K, [&](int) { return b; }, b);
-    multiply<T, S, DIRECT>(acc, oa, ob, steps(K), 0, lds, [&](int j) { return (wn * S::NF + j) * 16; }, [] {});
-    const tbe_stack& o = which == 0 ? g.o0 : which == 1 ? g.o1 : g.o2;
-    T* out = static_cast<T*>(o.data) + (int64_t)s.e * o.stride;
-#pragma unroll
-    for (int i = 0; i < S::MF; ++i) {
-      const int32_t m = m0 + (wm * S::MF + i) * 16 + lane % 16;
-      if (m >= rows) continue;
-#pragma unroll
-      for (int j = 0; j < S::NF; j += 2) {
-        const int32_t n = n0 + (wn * S::NF + j) * 16 + lane / 16 * 8;
-        float f[8];
-        eight(acc[i][j], acc[i][j + 1], f);
-        if (n < cols) store8<T>(out + (int64_t)m * o.ld + n, cols - n, f);
-      }
-    }
-    return;
-  } else {
-    Span s;
-    if (!find_block<S::BM>(g.offsets, g.E, g.M, g.nt, (int32_t)tile, s)) return;
-    // an expert's tiles in groups of 8 blocks of rows, in a group the rows first: the
-    // 32 tiles that an XCD works on share rows and matrices in its L2
-    constexpr int GROUP = 8;
-    const int32_t group = s.place / (GROUP * g.nt) * GROUP;
-    const int32_t high = min(GROUP, s.tiles - group), in = s.place - group * g.nt;
-    const int32_t m0 = s.first + (group + in % high) * S::BM;
-    // columns of a tile: of Up's two products half each
-    constexpr int BN = P == Up ? S::BN / 2 : S::BN;
-    const int32_t n0 = in / high * BN;
-    const int32_t N = P == Up || P == Dh ? g.F : g.D;
-    const T* a = static_cast<const T*>(g.a) + (int64_t)m0 * g.lda;
-    const int32_t last = s.end - 1 - m0;
-    const int32_t K = P == Up || P == Dh ? g.D : g.F;
-    Operand<T, Along, S::BM, S::NT, DIRECT> oa;
-    oa.start(S::BM, g.lda, K, [&](int r) { return a + (int64_t)min(r, last) * g.lda; }, a);
-    Operand<T, P == Up || P == Down ? Along : Across, S::BN, S::NT, DIRECT, P == Up> ob;
-    const T* b0 = matrix<T>(g.b0, s.e);
-    constexpr int HALF = S::NF / 2;
-    auto row_b = [&](int j) { return (wn * S::NF + j) * 16; };
-    if constexpr (P == Up) {
-      static_assert(S::NF % 2 == 0, "both products in one wave");
-      const T* b1 = matrix<T>(g.b1, s.e);
-      b0 += (int64_t)n0 * g.b0.ld;
-      b1 += (int64_t)n0 * g.b1.ld;
-      ob.start(S::BN, 0, K, [&](int r) {   // rows of up behind those of gate
-        const int64_t n = min(column_of(r < BN ? r : r - BN), N - 1 - n0);
-        return r < BN ? b0 + n * g.b0.ld : b1 + n * g.b1.ld;
-      }, b0, b1);
-      multiply<T, S, DIRECT>(acc, oa, ob, steps(K), 0, lds, [&](int j) {
-        return j < HALF ? (wn * HALF + j) * 16 : BN + (wn * HALF + j - HALF) * 16;
-      }, [] {});
-    } else if constexpr (P == Down) {
-      b0 += (int64_t)n0 * g.b0.ld;
-      ob.start(S::BN, 0, K, [&](int r) { return b0 + (int64_t)min(column_of(r), N - 1 - n0) * g.b0.ld; }, b0);
-      multiply<T, S, DIRECT>(acc, oa, ob, steps(K), 0, lds, row_b, [] {});
+// Workgroups stay, and take tiles by XCD: each XCD has a run of neighbouring tiles,
+// its workgroups neighbours in it at any time.
+template <typename T, Product P, class S, bool DIRECT>
+__global__ __launch_bounds__(S::NT, 2) void ffn_kernel(Args g) {
+  __shared__ __attribute__((aligned(16))) char lds[2 * S::AREA];
+  constexpr int BK = kStepBytes / (int)sizeof(T);
+  // columns of a tile: of Up's two products half each
+  constexpr int BN = P == Up ? S::BN / 2 : S::BN, HALF = S::NF / 2, COLS = P == Up ? HALF : S::NF;
+  static_assert(COLS % 2 == 0, "fragments in pairs");
+  int64_t all = g.tiles;
+  if constexpr (P != Dw) all = (int64_t)count_blocks<S::BM>(g.offsets, g.E, g.M) * g.nt;
+  const int64_t per = (all + kXcds - 1) / kXcds;
+  const int64_t begin = blockIdx.x % kXcds * per, end = begin + per < all ? begin + per : all;
+  int64_t at = begin + blockIdx.x / kXcds;
+  const int64_t stride = gridDim.x / kXcds;
+
+  auto locate = [&](int64_t tile) {
+    Tile t;
+    if constexpr (P == Dw) {
+      // tiles of one expert: gate's, up's, down's
+      const int32_t ft = (g.F + S::BM - 1) / S::BM, dt = (g.D + S::BN - 1) / S::BN;
+      const int32_t dt2 = (g.D + S::BM - 1) / S::BM, ft2 = (g.F + S::BN - 1) / S::BN;
+      const int32_t each = ft * dt, one = 2 * each + dt2 * ft2;
+      Span s;
+      expert_rows(g.offsets, (int32_t)(tile / one), g.M, s);
+      const int32_t in = (int32_t)(tile % one);
+      t.which = in < each ? 0 : in < 2 * each ? 1 : 2;
+      const int32_t across = t.which == 2 ? ft2 : dt, place = in - t.which * each;
+      t.m0 = place / across * S::BM;
+      t.n0 = place % across * S::BN;
+      t.rows = t.which == 2 ? g.D : g.F;
+      t.cols = t.which == 2 ? g.F : g.D;
+      t.e = s.e;
+      t.first = s.first;
+      t.K = s.end - s.first;
     } else {
-      b0 += n0;
-      ob.start(N - n0, g.b0.ld, K, [&](int) { return b0; }, b0);
-      if constexpr (P == Dh) {
-        multiply<T, S, DIRECT>(acc, oa, ob, steps(K), 0, lds, row_b, [] {});
+      Span s = {};
+      find_block<S::BM>(g.offsets, g.E, g.M, g.nt, (int32_t)tile, s);
+      // an expert's tiles in groups of 8 blocks of rows, in a group the rows first: the
+      // 32 tiles that an XCD works on share rows and matrices in its L2
+      constexpr int GROUP = 8;
+      const int32_t group = s.place / (GROUP * g.nt) * GROUP;
+      const int32_t high = min(GROUP, s.tiles - group), in = s.place - group * g.nt;
+      t.m0 = s.first + (group + in % high) * S::BM;
+      t.n0 = in / high * BN;
+      t.rows = s.end;
+      t.cols = P == Up || P == Dh ? g.F : g.D;
+      t.K = P == Up || P == Dh ? g.D : g.F;
+      t.e = s.e;
+      t.which = 0;
+    }
+    return t;
+  };
+  using OA = Operand<T, P == Dw ? Across : Along, S::BM, S::NT, DIRECT>;
+  using OB = Operand<T, P == Up || P == Down ? Along : Across, S::BN, S::NT, DIRECT, P == Up>;
+  Walk<T, S, DIRECT, OA, OB> w;
+  w.lds = lds;
+  // Sets the operands to a tile; part 1 of Dx is up's.
+  auto set = [&](const Tile& t, int part) {
+    if constexpr (P == Dw) {
+      const bool down = t.which == 2;
+      const int64_t lda = down ? g.lddys : g.lda, ldb = down ? g.ldh : g.ldxs;
+      const T* a = static_cast<const T*>(down ? g.dys : g.a) + (t.which == 1 ? g.half : 0) + t.first * lda + t.m0;
+      const T* b = static_cast<const T*>(down ? g.h : g.xs) + t.first * ldb + t.n0;
+      w.a.start(t.rows - t.m0, lda, t.K, [&](int) { return a; }, a);
+      w.b.start(t.cols - t.n0, ldb, t.K, [&](int) { return b; }, b);
+    } else {
+      const T* a = static_cast<const T*>(g.a) + (int64_t)t.m0 * g.lda + (part ? g.half : 0);
+      const int32_t last = t.rows - 1 - t.m0, right = t.cols - 1 - t.n0;
+      w.a.start(S::BM, g.lda, t.K, [&](int r) { return a + (int64_t)min(r, last) * g.lda; }, a);
+      const tbe_stack& m = part ? g.b1 : g.b0;
+      if constexpr (P == Up) {   // rows of up behind those of gate
+        const T *b0 = matrix<T>(g.b0, t.e) + t.n0 * g.b0.ld, *b1 = matrix<T>(g.b1, t.e) + t.n0 * g.b1.ld;
+        w.b.start(S::BN, 0, t.K, [&](int r) {
+          return r < BN ? b0 + min(r, right) * g.b0.ld : b1 + min(r - BN, right) * g.b1.ld;
+        }, b0, b1);
+      } else if constexpr (P == Down) {
+        const T* b = matrix<T>(m, t.e) + t.n0 * m.ld;
+        w.b.start(S::BN, 0, t.K, [&](int r) { return b + min(r, right) * m.ld; }, b);
       } else {
-        multiply<T, S, DIRECT>(acc, oa, ob, steps(K), steps(K), lds, row_b, [&] {
-          const T *a1 = a + g.half, *b1 = matrix<T>(g.b1, s.e) + n0;
-          oa.start(S::BM, g.lda, K, [&](int r) { return a1 + (int64_t)min(r, last) * g.lda; }, a1);
-          ob.start(N - n0, g.b1.ld, K, [&](int) { return b1; }, b1);
-        });
+        const T* b = matrix<T>(m, t.e) + t.n0;
+        w.b.start(t.cols - t.n0, m.ld, t.K, [&](int) { return b; }, b);
       }
     }
-    // eight columns of a row at a time; Dh's rows of `pre` are loaded two ahead of
-    // the stores, which may go to the same memory for all the compiler knows
-    constexpr int COLS = P == Up ? HALF : S::NF;
+  };
+  auto steps = [](int32_t k) { return (k + BK - 1) / BK; };
+  auto row_b = [&](int j) {
+    const int wn = wave_index() % S::WN;
+    if constexpr (P == Up) return j < HALF ? (wn * HALF + j) * 16 : BN + (wn * HALF + j - HALF) * 16;
+    else return (wn * S::NF + j) * 16;
+  };
+
+  if (at >= end) return;
+  Tile t = locate(at);
+  set(t, 0);
+  if (t.K > 0) w.fetch();
+  for (; at < end; at += stride) {
+    f32x4 acc[S::MF][S::NF];
+#pragma unroll
+    for (int i = 0; i < S::MF; ++i)
+#pragma unroll
+      for (int j = 0; j < S::NF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const Tile now = t;
+    w.multiply(acc, steps(now.K), P == Dx ? steps(now.K) : 0, row_b, [&] { set(now, 1); }, [&] {
+      if (at + stride >= end) return;
+      t = locate(at + stride);
+      set(t, 0);
+      if (t.K > 0) w.fetch();
+    });
+
+    // eight columns of a row at a time; Dh's rows of `pre` are loaded two ahead of the
+    // stores, which may go to the same memory for all the compiler knows
     constexpr int AHEAD = P == Dh ? 2 : 1;
-    static_assert(S::MF % AHEAD == 0 && COLS % 2 == 0, "whole groups");
-    const int32_t nw = n0 + wn * COLS * 16 + lane / 16 * 8;
+    static_assert(S::MF % AHEAD == 0, "whole groups");
+    const int thread = thread_again(), lane = thread % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(thread / kWave), wm = wave / S::WN, wn = wave % S::WN;
+    const int32_t N = now.cols, nw = now.n0 + wn * COLS * 16 + eight_at(lane);
 #pragma unroll
     for (int i0 = 0; i0 < S::MF; i0 += AHEAD) {
       [[maybe_unused]] typename Pack<T, 8>::raw pu[AHEAD][COLS / 2], pv[AHEAD][COLS / 2];
       if constexpr (P == Dh) {
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-          const int32_t m = m0 + (wm * S::MF + i0 + i) * 16 + lane % 16;
+          const int32_t m = now.m0 + (wm * S::MF + i0 + i) * 16 + lane % 16;
           const T* pre = static_cast<const T*>(g.pre) + (int64_t)m * g.ldpre;
 #pragma unroll
           for (int j = 0; j < COLS; j += 2) {
             const int32_t n = nw + j * 16;
-            pu[i][j / 2] = load8<T>(pre + n, m < s.end ? N - n : 0);
-            pv[i][j / 2] = load8<T>(pre + N + n, m < s.end ? N - n : 0);
+            pu[i][j / 2] = load8<T>(pre + n, m < now.rows ? N - n : 0);
+            pv[i][j / 2] = load8<T>(pre + N + n, m < now.rows ? N - n : 0);
           }
         }
       }
 #pragma unroll
       for (int i = i0; i < i0 + AHEAD; ++i) {
-        const int32_t m = m0 + (wm * S::MF + i) * 16 + lane % 16;
-        if (m >= s.end) continue;
-        T* c = static_cast<T*>(g.c) + (int64_t)m * g.ldc;
-        T* c2 = static_cast<T*>(g.c2) + (int64_t)m * g.ldc2;
+        const int32_t m = now.m0 + (wm * S::MF + i) * 16 + lane % 16;
+        const bool in = m < now.rows;
+        T *c, *c2 = nullptr;
+        if constexpr (P == Dw) {
+          const tbe_stack& o = now.which == 0 ? g.o0 : now.which == 1 ? g.o1 : g.o2;
+          c = static_cast<T*>(o.data) + now.e * o.stride + m * o.ld;
+        } else {
+          c = static_cast<T*>(g.c) + m * g.ldc;
+          c2 = static_cast<T*>(g.c2) + m * g.ldc2;
+        }
 #pragma unroll
         for (int j = 0; j < COLS; j += 2) {
           const int32_t n = nw + j * 16;
-          if (n >= N) continue;
           float f[8];
-          eight(acc[i][j], acc[i][j + 1], f);
+          eight(acc[i][j], acc[i][j + 1], f);   // (all lanes)
+          [[maybe_unused]] float u[8], v[8];
+          if constexpr (P == Up) eight(acc[i][j + HALF], acc[i][j + HALF + 1], u);
+          if (!in || n >= N) continue;
           if constexpr (P == Up) {
-            float u[8];
-            eight(acc[i][j + HALF], acc[i][j + HALF + 1], u);
             if (g.c2) {
               store8<T>(c2 + n, N - n, f);
               store8<T>(c2 + N + n, N - n, u);
             }
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-              float a, da;
-              activate<T>(g.act, f[q], a, da);
-              f[q] = a * u[q];
+              float x, da;
+              activate<T>(g.act, f[q], x, da);
+              f[q] = x * u[q];
             }
           } else if constexpr (P == Dh) {
-            float u[8], v[8];
             widen<T, 8>(pu[i - i0][j / 2], u);
             widen<T, 8>(pv[i - i0][j / 2], v);
 #pragma unroll
@@ -276,7 +293,9 @@ hipError_t launch(Args g, bool direct, hipStream_t s) {
     // every expert may end in a part of a block
     g.tiles = (g.M / S::BM + std::min(g.E, g.M)) * (int64_t)g.nt;
   }
-  const unsigned grid = (unsigned)xcd_grid(g.tiles);
+  // as many workgroups as find room at once, a multiple of the XCDs
+  constexpr int64_t kRoom = 256 * (2 * S::AREA > (80 << 10) ? 1 : 2);
+  const unsigned grid = (unsigned)std::min(xcd_grid(g.tiles), kRoom);
   if (direct) ffn_kernel<T, P, S, true><<<grid, S::NT, 0, s>>>(g);
   else if constexpr (S::NT == 256) ffn_kernel<T, P, S, false><<<grid, S::NT, 0, s>>>(g);
   return hipGetLastError();

@@ -9,8 +9,8 @@
 //
 // In LDS a 16-byte piece stands at a place permuted by its row, so that the
 // lanes of one read meet different banks. The wave multiplies B by A: a lane
-// then holds four columns of one row of C from each fragment, and as two
-// fragments take the fours of 32 columns in turn, eight neighbouring ones.
+// then holds four neighbouring columns of one row of C from each fragment; lanes
+// exchange half of two fragments' for eight neighbouring ones (eight()).
 #pragma once
 
 #include "lm.h"
@@ -49,23 +49,39 @@ template <> struct Mma<float> {   // a lane's four elements of k: one product ea
 
 enum Layout { Along, Across };
 
+// The thread's index, unknown to the compiler from here on: what is formed from it is
+// formed here, and holds no registers through the products before.
+__device__ __forceinline__ int thread_again() {
+  int t = (int)threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
+
 // Byte offset of a piece in LDS. Along: row r, piece c of 8.
 __device__ __forceinline__ uint32_t along_at(int r, int c) {
   return (uint32_t)(r * kStepBytes + ((c ^ ((r >> 1) & 7)) << 4));
 }
-// The column that row r of B's tile holds: of 32, rows 0-15 take the first four of
-// each eight, rows 16-31 the others.
-__device__ __forceinline__ int column_of(int r) {
-  return (r & ~31) | ((r & 12) << 1) | ((r & 16) >> 2) | (r & 3);
-}
-// Across: row k, byte b of BYTES; 64-byte units are permuted: by k mod 4 for 16
-// bits, whose transposing reads take four rows at a time; by k / 4 for float32,
-// where the four rows of one read are 4 apart.
+// Across: row k, byte b of BYTES; 32-byte units are permuted: by k mod 4 and k / 8
+// for 16 bits, whose transposing reads take four rows and the four 8 further on at
+// a time; in pairs by k / 4 for float32, where the four rows of one read are 4 apart.
 template <typename T, int BYTES>
 __device__ __forceinline__ uint32_t across_at(int k, int b) {
-  const int f = sizeof(T) == 2 ? k & 3 : (k >> 2) & 3;
-  return (uint32_t)(k * BYTES + ((((b >> 6) ^ f) & (BYTES / 64 - 1)) << 6) + (b & 63));
+  const int f = sizeof(T) == 2 ? (k & 3) | ((k >> 1) & 4) : ((k >> 2) & 3) << 1;
+  return (uint32_t)(k * BYTES + ((((b >> 5) ^ f) & (BYTES / 32 - 1)) << 5) + (b & 31));
 }
+
+// Eight neighbouring columns of a row of C from two fragments of 16 columns: lanes of
+// even sixteens take the first fragment's, the others the second's, of the 16 columns
+// the half that (lane / 32) says.
+__device__ __forceinline__ void eight(const f32x4& p, const f32x4& q, float (&f)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(p[j]), __float_as_uint(q[j]), false, false);
+    f[j] = __uint_as_float(r[0]);
+    f[j + 4] = __uint_as_float(r[1]);
+  }
+}
+__device__ __forceinline__ int eight_at(int lane) { return (lane & 16) + (lane & 32) / 4; }
 
 // One operand's pieces of a step, from memory to LDS. ROWS: of the tile, NT:
 // threads. DIRECT: every piece lies in its matrix whole and aligned, and goes to
@@ -93,8 +109,8 @@ struct Operand {
 
   // Piece i of this thread: row (of the tile, or of k) and column in pieces. Direct
   // pieces are written in the order of threads, so it is the source that is permuted.
-  static __device__ __forceinline__ void place(int i, int& row, int& col) {
-    const int at = (int)threadIdx.x + i * NT;
+  static __device__ __forceinline__ void place(int thread, int i, int& row, int& col) {
+    const int at = thread + i * NT;
     if constexpr (L == Along) {
       row = at / 8;
       col = DIRECT ? (at % 8) ^ ((row >> 1) & 7) : at % 8;
@@ -116,10 +132,11 @@ struct Operand {
     base[0] = first;
     if constexpr (SPLIT) base[1] = second;
     step = L == Along ? BK : BK * ld;
+    const int thread = thread_again();
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
       int q, c;
-      place(i, q, c);
+      place(thread, i, q, c);
       const T* from = L == Along ? row(q) + c * VE : row(0) + (int64_t)q * ld + c * VE;
       if constexpr (DIRECT) {
         off[i] = (uint32_t)((from - (SPLIT && i >= PIECES / 2 ? second : first)) * (int64_t)sizeof(T));
@@ -143,21 +160,25 @@ struct Operand {
                  (int)kOutside, 0x00020000};
       base[j] += step;
     }
-    const bool whole = left >= BK;
     const uint32_t to = __builtin_amdgcn_readfirstlane(lds + wave_index() * (kWave * 16));
-#pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-      uint32_t from = off[i];
-      if (!whole) {
-        int q, c;
-        place(i, q, c);
-        if ((L == Along ? c * VE : q) >= left) from = kOutside;
-      }
+    auto one = [&](int i, uint32_t from) {
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"   // m0 is reserved: the compiler keeps nothing in it
       asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                    :: "s"(to + i * (NT * 16)), "v"(from), "s"(rsrc[SPLIT && i >= PIECES / 2 ? 1 : 0]) : "m0");
 #pragma clang diagnostic pop
+    };
+    if (left >= BK) {
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) one(i, off[i]);
+    } else {
+      const int thread = thread_again();
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        int q, c;
+        place(thread, i, q, c);
+        one(i, (L == Along ? c * VE : q) >= left ? kOutside : off[i]);
+      }
     }
     left -= BK;
   }
@@ -167,7 +188,7 @@ struct Operand {
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
       int q, c;
-      place(i, q, c);
+      place((int)threadIdx.x, i, q, c);
       // elements of the piece that exist
       const int n = L == Along ? left - c * VE : q < left ? limit - c * VE : 0;
       r[i] = make_uint4(0, 0, 0, 0);
@@ -187,37 +208,47 @@ struct Operand {
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
       int q, c;
-      place(i, q, c);
+      place((int)threadIdx.x, i, q, c);
       *reinterpret_cast<uint4*>(lds + (L == Along ? along_at(q, c) : across_at<T, BYTES>(q, c * 16))) = r[i];
     }
   }
 
-  // A lane's part of 16 rows of the tile from `row`: row + lane % 16 (column_of it
-  // where the tile is Across and PERMUTE), and of half step s (64 bytes of k) the
-  // quarter lane / 16.
-  template <bool PERMUTE>
-  static __device__ __forceinline__ uint4 frag(const char* lds, int row, int s) {
+  // Where a lane reads its part of rows: of row lane % 16, and of half step s (64
+  // bytes of k) the quarter lane / 16; other rows differ by a known number. (Unknown
+  // to the compiler, which would otherwise keep an address for each fragment in
+  // registers that the products need.)
+  typedef __attribute__((address_space(3))) const char* lds_ptr;
+  static __device__ __forceinline__ uint32_t lane_at(const char* lds, int s) {
     const int lane = lane_id();
+    uint32_t at;
+    if constexpr (L == Along) at = along_at(lane % 16, s * 4 + lane / 16);
+    else if constexpr (sizeof(T) == 2)   // of 16 lanes, lane i asks for row i / 4, columns i % 4 * 4 on; it gets column i
+      at = across_at<T, BYTES>(s * 32 + lane / 16 * 8 + lane % 16 / 4, lane % 4 * 8);
+    else at = across_at<T, BYTES>(s * 16 + lane / 16 * 4, lane % 16 * 4);
+    at += (uint32_t)(uintptr_t)(lds_ptr)lds;
+    if constexpr (L == Across) asm volatile("" : "+v"(at));
+    return at;
+  }
+  // A lane's part of the 16 rows from `row`.
+  static __device__ __forceinline__ uint4 frag(uint32_t at, int row) {
     if constexpr (L == Along) {
-      return *reinterpret_cast<const uint4*>(lds + along_at(row + lane % 16, s * 4 + lane / 16));
-    } else if constexpr (sizeof(T) == 2) {
-      // of 16 lanes, lane i asks for row i / 4, columns i % 4 * 4 on; it gets column i
-      typedef short s16x4 __attribute__((ext_vector_type(4)));
-      typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-      const int k = s * 32 + lane / 16 * 8 + lane % 16 / 4;
-      const int b = (PERMUTE ? (row & ~31) + lane % 4 * 8 + (row & 16) / 4 : row + lane % 4 * 4) * 2;
-      union { s16x4 h[2]; uint4 u; } v;
-      v.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lds + across_at<T, BYTES>(k, b)));
-      v.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lds + across_at<T, BYTES>(k + 4, b)));
-      return v.u;
+      typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) const u32x4* ptr;
+      return __builtin_bit_cast(uint4, *(ptr)(uintptr_t)(at + row * kStepBytes));
     } else {
-      uint32_t v[4];
-      const int col = PERMUTE ? column_of(row + lane % 16) : row + lane % 16;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[j] = *reinterpret_cast<const uint32_t*>(
-            lds + across_at<T, BYTES>(s * 16 + lane / 16 * 4 + j, col * 4));
-      return make_uint4(v[0], v[1], v[2], v[3]);
+      at ^= row * (int)sizeof(T);   // (units are permuted by the same pattern in all columns)
+      if constexpr (sizeof(T) == 2) {
+        typedef short s16x4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) s16x4* ptr;
+        union { s16x4 h[2]; uint4 u; } v;
+        v.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(uintptr_t)at);
+        v.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(uintptr_t)(at + 4 * BYTES));
+        return v.u;
+      } else {
+        typedef __attribute__((address_space(3))) const uint32_t* ptr;
+        const ptr p = (ptr)(uintptr_t)at;
+        return make_uint4(p[0], p[BYTES / 4], p[BYTES / 2], p[3 * BYTES / 4]);
+      }
     }
   }
 };
@@ -237,10 +268,11 @@ struct Frags {
   template <class A, class B, typename RowB>
   __device__ __forceinline__ void read(const char* lds, int s, RowB row_b) {
     const int wm = wave_index() / S::WN;
+    const uint32_t at_a = A::lane_at(lds, s), at_b = B::lane_at(lds + S::BM * kStepBytes, s);
 #pragma unroll
-    for (int j = 0; j < S::NF; ++j) b[j] = B::template frag<true>(lds + S::BM * kStepBytes, row_b(j), s);
+    for (int j = 0; j < S::NF; ++j) b[j] = B::frag(at_b, row_b(j));
 #pragma unroll
-    for (int i = 0; i < S::MF; ++i) a[i] = A::template frag<false>(lds, (wm * S::MF + i) * 16, s);
+    for (int i = 0; i < S::MF; ++i) a[i] = A::frag(at_a, (wm * S::MF + i) * 16);
   }
   template <typename T>
   __device__ __forceinline__ void mul(f32x4 (&acc)[S::MF][S::NF]) const {
@@ -263,80 +295,102 @@ __device__ __forceinline__ void interleave() {
   __builtin_amdgcn_sched_group_barrier(0x008, PRODUCTS - READS * EACH, 0);
 }
 
-// acc += the product over the steps of k: `steps` of the operands as they are,
-// then `more` after turn(). `row_b(nf)`: first of the 16 rows of B's tile that
-// fragment nf of this wave takes.
+// The products of a workgroup's tiles, one after the other.
 //
 // Direct: behind the barrier of step i its data are in one area of LDS and no wave
-// reads the other any more. A wave then multiplies the second half of step i - 1,
-// which it has in registers, while it reads the first half of step i, and so on:
-// reads of LDS and products always have each other to run beside.
-template <typename T, class S, bool DIRECT, class A, class B, typename RowB, typename Turn>
-__device__ __forceinline__ void multiply(f32x4 (&acc)[S::MF][S::NF], A& a, B& b, int steps, int more,
-                                         char* lds, RowB row_b, Turn turn) {
-  const int all = steps + more;
-  if (all == 0) return;
-  if constexpr (DIRECT) {
-    constexpr int kReads = S::MF * A::READS + S::NF * B::READS;
-    constexpr int kProducts = S::MF * S::NF * (sizeof(T) == 4 ? 4 : 1);
+// reads the other any more, so step i + 1 is asked of memory into that. A wave then
+// multiplies the second half of step i - 1, which it has in registers, while it reads
+// the first half of step i, and so on: loads, reads of LDS and products always have
+// each other to run beside. What is done with a tile's result runs while the next
+// tile's first step is on its way (`next`).
+template <typename T, class S, bool DIRECT, class A, class B>
+struct Walk {
+  char* lds;
+  uint32_t area = 0;   // of the next step
+  A a;
+  B b;
+
+  __device__ __forceinline__ void arrived() const {
     typedef __attribute__((address_space(3))) char* lds_ptr;
-    const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr)lds;
-    auto arrived = [&]() {
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" :: "s"(base) : "memory");
-    };
-    auto fetch = [&](int i) {
-      if (i == steps) turn();
-      const uint32_t to = base + (i & 1) * S::AREA;
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" :: "s"((uint32_t)(uintptr_t)(lds_ptr)lds) : "memory");
+  }
+  __device__ __forceinline__ void fetch() {
+    if constexpr (DIRECT) {
+      typedef __attribute__((address_space(3))) char* lds_ptr;
+      const uint32_t to = (uint32_t)(uintptr_t)(lds_ptr)lds + area;
       a.fetch(to);
       b.fetch(to + S::BM * kStepBytes);
-    };
-    Frags<S> even, odd;
-    fetch(0);
-    arrived();
-    if (all > 1) fetch(1);
-    even.template read<A, B>(lds, 0, row_b);
-    odd.template read<A, B>(lds, 1, row_b);
-    even.template mul<T>(acc);
-    for (int i = 1; i < all; ++i) {
-      arrived();
-      if (i + 1 < all) fetch(i + 1);
-      const char* now = lds + (i & 1) * S::AREA;
-      even.template read<A, B>(now, 0, row_b);
-      odd.template mul<T>(acc);
-      interleave<kReads, kProducts>();
-      odd.template read<A, B>(now, 1, row_b);
-      even.template mul<T>(acc);
-      interleave<kReads, kProducts>();
-    }
-    odd.template mul<T>(acc);
-  } else {
-    auto load = [&](int i) {
-      if (i == steps) turn();
-      a.load();
-      b.load();
-    };
-    load(0);
-    a.store(lds);
-    b.store(lds + S::BM * kStepBytes);
-    __syncthreads();
-    for (int i = 0; i < all; ++i) {
-      const char* now = lds + (i & 1) * S::AREA;
-      if (i + 1 < all) load(i + 1);
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        Frags<S> f;
-        f.template read<A, B>(now, s, row_b);
-        f.template mul<T>(acc);
-      }
-      if (i + 1 < all) {
-        char* next = lds + (~i & 1) * S::AREA;
-        a.store(next);
-        b.store(next + S::BM * kStepBytes);
-      }
-      __syncthreads();
+      area ^= S::AREA;
     }
   }
-}
+
+  // acc += the product over `steps` steps of the operands as they are and `more` after
+  // turn(). row_b(nf): first of the 16 rows of B's tile that fragment nf of this wave
+  // takes. next(): sets the operands to the next tile and fetches its first step.
+  // The first step of this tile has been fetched.
+  template <typename RowB, typename Turn, typename Next>
+  __device__ __forceinline__ void multiply(f32x4 (&acc)[S::MF][S::NF], int steps, int more, RowB row_b,
+                                           Turn turn, Next next) {
+    const int all = steps + more;
+    if constexpr (DIRECT) {
+      constexpr int kReads = S::MF * A::READS + S::NF * B::READS;
+      constexpr int kProducts = S::MF * S::NF * (sizeof(T) == 4 ? 4 : 1);
+      if (all == 0) return next();
+      Frags<S> even, odd;
+      const char* now = lds + (area ^ S::AREA);
+      arrived();
+      if (1 == steps && more > 0) turn();
+      if (all > 1) fetch();
+      even.template read<A, B>(now, 0, row_b);
+      odd.template read<A, B>(now, 1, row_b);
+      even.template mul<T>(acc);
+      for (int i = 1; i < all; ++i) {
+        now = lds + (area ^ S::AREA);
+        arrived();
+        if (i + 1 == steps && more > 0) turn();
+        if (i + 1 < all) fetch();
+        even.template read<A, B>(now, 0, row_b);
+        odd.template mul<T>(acc);
+        interleave<kReads, kProducts>();
+        odd.template read<A, B>(now, 1, row_b);
+        even.template mul<T>(acc);
+        interleave<kReads, kProducts>();
+      }
+      odd.template mul<T>(acc);
+      next();
+    } else {
+      auto load = [&](int i) {
+        if (i == steps && more > 0) turn();
+        a.load();
+        b.load();
+      };
+      if (all > 0) {
+        load(0);
+        __syncthreads();   // the last tile's readers are done
+        a.store(lds);
+        b.store(lds + S::BM * kStepBytes);
+        __syncthreads();
+      }
+      for (int i = 0; i < all; ++i) {
+        const char* now = lds + (i & 1) * S::AREA;
+        if (i + 1 < all) load(i + 1);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          Frags<S> f;
+          f.template read<A, B>(now, s, row_b);
+          f.template mul<T>(acc);
+        }
+        if (i + 1 < all) {
+          char* then = lds + (~i & 1) * S::AREA;
+          a.store(then);
+          b.store(then + S::BM * kStepBytes);
+        }
+        __syncthreads();
+      }
+      next();
+    }
+  }
+};
 
 // The experts' rows, from the offsets: each is at least its predecessor and in
 // [0, M], whatever the memory holds. Uniform over the wave.
@@ -363,6 +417,24 @@ __device__ __forceinline__ int32_t wave_scan_sum(int32_t x) {
   return x;
 }
 
+// Blocks of BM rows of all experts.
+template <int BM>
+__device__ __forceinline__ int32_t count_blocks(const int32_t* __restrict__ offsets, int32_t E, int32_t M) {
+  int32_t all = 0, low = 0;
+  for (int32_t e0 = 0; e0 < E; e0 += kWave) {
+    const int32_t e = e0 + lane_id();
+    int32_t a = min(max(offsets[min(e, E)], 0), M);
+    int32_t z = min(max(offsets[min(e + 1, E)], 0), M);
+    a = max(wave_scan_max(a), low);
+    z = max(a, z);
+    all += (z - a + BM - 1) / BM;
+    low = __builtin_amdgcn_readlane(z, kWave - 1);
+  }
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) all += __shfl_xor(all, d);
+  return __builtin_amdgcn_readfirstlane(all);
+}
+
 // Block `tile` of the experts' rows in blocks of BM, nt of them side by side: an
 // expert's blocks are neighbours. False behind the last.
 template <int BM>
@@ -372,11 +444,11 @@ __device__ __forceinline__ bool find_block(const int32_t* __restrict__ offsets, 
   int32_t before = 0, low = 0;
   for (int32_t e0 = 0; e0 < E; e0 += kWave) {
     const int32_t e = e0 + lane_id();
-    int32_t a = e <= E ? min(max(offsets[min(e, E)], 0), M) : 0;
-    int32_t z = e < E ? min(max(offsets[e + 1], 0), M) : 0;
+    int32_t a = min(max(offsets[min(e, E)], 0), M);
+    int32_t z = min(max(offsets[min(e + 1, E)], 0), M);
     a = max(wave_scan_max(a), low);
     z = max(a, z);
-    const int32_t tiles = e < E ? (z - a + BM - 1) / BM : 0;
+    const int32_t tiles = (z - a + BM - 1) / BM;
     const int32_t upto = before + wave_scan_sum(tiles);
     const uint64_t hit = __ballot(upto > want);
     if (hit) {
