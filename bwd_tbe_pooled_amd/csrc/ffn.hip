@@ -12,6 +12,7 @@
 // waits for the host; workgroups beyond the last tile end at once. A tile's rows
 // are one expert's: rows behind its end repeat its last row and are not stored.
 #include <algorithm>
+#include <type_traits>
 
 #include "ffn_tile.h"
 
@@ -102,8 +103,9 @@ __global__ __launch_bounds__(S::NT, 2) void ffn_kernel(Args g) {
   // columns of a tile: of Up's two products half each
   constexpr int BN = P == Up ? S::BN / 2 : S::BN, HALF = S::NF / 2, COLS = P == Up ? HALF : S::NF;
   static_assert(COLS % 2 == 0, "fragments in pairs");
-  int64_t all = g.tiles;
-  if constexpr (P != Dw) all = (int64_t)count_blocks<S::BM>(g.offsets, g.E, g.M) * g.nt;
+  __shared__ Spans spans;
+  spans.fill<S::BM>(g.offsets, g.E, g.M);
+  const int64_t all = P == Dw ? g.tiles : (int64_t)spans.upto[g.E - 1] * g.nt;
   const int64_t per = (all + kXcds - 1) / kXcds;
   const int64_t begin = blockIdx.x % kXcds * per, end = begin + per < all ? begin + per : all;
   int64_t at = begin + blockIdx.x / kXcds;
@@ -116,8 +118,7 @@ __global__ __launch_bounds__(S::NT, 2) void ffn_kernel(Args g) {
       const int32_t ft = (g.F + S::BM - 1) / S::BM, dt = (g.D + S::BN - 1) / S::BN;
       const int32_t dt2 = (g.D + S::BM - 1) / S::BM, ft2 = (g.F + S::BN - 1) / S::BN;
       const int32_t each = ft * dt, one = 2 * each + dt2 * ft2;
-      Span s;
-      expert_rows(g.offsets, (int32_t)(tile / one), g.M, s);
+      t.e = (int32_t)(tile / one);
       const int32_t in = (int32_t)(tile % one);
       t.which = in < each ? 0 : in < 2 * each ? 1 : 2;
       const int32_t across = t.which == 2 ? ft2 : dt, place = in - t.which * each;
@@ -125,23 +126,23 @@ __global__ __launch_bounds__(S::NT, 2) void ffn_kernel(Args g) {
       t.n0 = place % across * S::BN;
       t.rows = t.which == 2 ? g.D : g.F;
       t.cols = t.which == 2 ? g.F : g.D;
-      t.e = s.e;
-      t.first = s.first;
-      t.K = s.end - s.first;
+      t.first = __builtin_amdgcn_readfirstlane(spans.first[t.e]);
+      t.K = __builtin_amdgcn_readfirstlane(spans.first[t.e + 1]) - t.first;
     } else {
-      Span s = {};
-      find_block<S::BM>(g.offsets, g.E, g.M, g.nt, (int32_t)tile, s);
+      t.e = __builtin_amdgcn_readfirstlane(spans.expert_of((int32_t)(tile / g.nt), g.E));
+      t.first = __builtin_amdgcn_readfirstlane(spans.first[t.e]);
+      t.rows = __builtin_amdgcn_readfirstlane(spans.first[t.e + 1]);
+      const int32_t blocks = (t.rows - t.first + S::BM - 1) / S::BM;
+      const int32_t place = (int32_t)tile - (__builtin_amdgcn_readfirstlane(spans.upto[t.e]) - blocks) * g.nt;
       // an expert's tiles in groups of 8 blocks of rows, in a group the rows first: the
       // 32 tiles that an XCD works on share rows and matrices in its L2
       constexpr int GROUP = 8;
-      const int32_t group = s.place / (GROUP * g.nt) * GROUP;
-      const int32_t high = min(GROUP, s.tiles - group), in = s.place - group * g.nt;
-      t.m0 = s.first + (group + in % high) * S::BM;
+      const int32_t group = place / (GROUP * g.nt) * GROUP;
+      const int32_t high = min(GROUP, blocks - group), in = place - group * g.nt;
+      t.m0 = t.first + (group + in % high) * S::BM;
       t.n0 = in / high * BN;
-      t.rows = s.end;
       t.cols = P == Up || P == Dh ? g.F : g.D;
       t.K = P == Up || P == Dh ? g.D : g.F;
-      t.e = s.e;
       t.which = 0;
     }
     return t;
@@ -196,86 +197,118 @@ __global__ __launch_bounds__(S::NT, 2) void ffn_kernel(Args g) {
 #pragma unroll
       for (int j = 0; j < S::NF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     const Tile now = t;
-    w.multiply(acc, steps(now.K), P == Dx ? steps(now.K) : 0, row_b, [&] { set(now, 1); }, [&] {
-      if (at + stride >= end) return;
-      t = locate(at + stride);
-      set(t, 0);
-      if (t.K > 0) w.fetch();
-    });
-
-    // eight columns of a row at a time; Dh's rows of `pre` are loaded two ahead of the
-    // stores, which may go to the same memory for all the compiler knows
-    constexpr int AHEAD = P == Dh ? 2 : 1;
+    // Dh's rows of `pre`, AHEAD at a time: a group is loaded before the stores of the group
+    // before it, the first one before the next tile's first step
+    constexpr int AHEAD = P == Dh ? 1 : S::MF, GROUPS = S::MF / AHEAD;
     static_assert(S::MF % AHEAD == 0, "whole groups");
-    const int thread = thread_again(), lane = thread % kWave;
-    const int wave = __builtin_amdgcn_readfirstlane(thread / kWave), wm = wave / S::WN, wn = wave % S::WN;
-    const int32_t N = now.cols, nw = now.n0 + wn * COLS * 16 + eight_at(lane);
-#pragma unroll
-    for (int i0 = 0; i0 < S::MF; i0 += AHEAD) {
-      [[maybe_unused]] typename Pack<T, 8>::raw pu[AHEAD][COLS / 2], pv[AHEAD][COLS / 2];
+    typedef typename Pack<T, 8>::raw Raw;
+    [[maybe_unused]] Raw kept[P == Dh ? 2 : 1][AHEAD][COLS / 2][2];
+    const bool whole = now.m0 + S::BM <= now.rows && now.n0 + BN <= now.cols;
+    auto load_kept = [&](int group) {
       if constexpr (P == Dh) {
+        const int thread = thread_again(), lane = thread % kWave;
+        const int wave = __builtin_amdgcn_readfirstlane(thread / kWave), wm = wave / S::WN, wn = wave % S::WN;
+        const int32_t nw = now.n0 + wn * COLS * 16 + eight_at(lane);
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-          const int32_t m = now.m0 + (wm * S::MF + i0 + i) * 16 + lane % 16;
-          const T* pre = static_cast<const T*>(g.pre) + (int64_t)m * g.ldpre;
+          const int32_t m = now.m0 + (wm * S::MF + group * AHEAD + i) * 16 + lane % 16;
+          const T* pre = static_cast<const T*>(g.pre) + m * g.ldpre + nw;
+#pragma unroll
+          for (int j = 0; j < COLS; j += 2) {
+            Raw(&r)[2] = kept[group & 1][i][j / 2];
+            if (whole) {
+              r[0] = load_pack<T, 8>(pre + j * 16);
+              r[1] = load_pack<T, 8>(pre + now.cols + j * 16);
+            } else {
+              const int32_t n = m < now.rows ? now.cols - nw - j * 16 : 0;
+              r[0] = load8<T>(pre + j * 16, n);
+              r[1] = load8<T>(pre + now.cols + j * 16, n);
+            }
+          }
+        }
+      }
+    };
+    w.multiply(acc, steps(now.K), P == Dx ? steps(now.K) : 0, row_b, [&] { set(now, 1); }, [&] {
+      load_kept(0);
+      if (at + stride < end) {
+        t = locate(at + stride);
+        set(t, 0);
+        if (t.K > 0) w.fetch();
+      }
+      asm volatile("" ::: "memory");   // the stores stay behind the fetch
+    });
+
+    // eight columns of a row at a time
+    auto finish = [&](auto is_whole) {
+      constexpr bool WHOLE = decltype(is_whole)::value;
+      const int thread = thread_again(), lane = thread % kWave;
+      const int wave = __builtin_amdgcn_readfirstlane(thread / kWave), wm = wave / S::WN, wn = wave % S::WN;
+      const int32_t N = now.cols, nw = now.n0 + wn * COLS * 16 + eight_at(lane);
+      auto put = [&](T* p, int32_t n, const float(&f)[8]) {
+        if constexpr (WHOLE) store_pack<T, 8>(p, narrow<T, 8>(f));
+        else store8<T>(p, n, f);
+      };
+#pragma unroll
+      for (int group = 0; group < GROUPS; ++group) {
+        if (group + 1 < GROUPS) load_kept(group + 1);
+#pragma unroll
+        for (int i = group * AHEAD; i < (group + 1) * AHEAD; ++i) {
+          const int32_t m = now.m0 + (wm * S::MF + i) * 16 + lane % 16;
+          const bool in = WHOLE || m < now.rows;
+          T *c, *c2 = nullptr;
+          if constexpr (P == Dw) {
+            const tbe_stack& o = now.which == 0 ? g.o0 : now.which == 1 ? g.o1 : g.o2;
+            c = static_cast<T*>(o.data) + now.e * o.stride + m * o.ld;
+          } else {
+            c = static_cast<T*>(g.c) + m * g.ldc;
+            c2 = static_cast<T*>(g.c2) + m * g.ldc2;
+          }
 #pragma unroll
           for (int j = 0; j < COLS; j += 2) {
             const int32_t n = nw + j * 16;
-            pu[i][j / 2] = load8<T>(pre + n, m < now.rows ? N - n : 0);
-            pv[i][j / 2] = load8<T>(pre + N + n, m < now.rows ? N - n : 0);
+            float f[8];
+            eight(acc[i][j], acc[i][j + 1], f);   // (all lanes)
+            [[maybe_unused]] float u[8], v[8];
+            if constexpr (P == Up) eight(acc[i][j + HALF], acc[i][j + HALF + 1], u);
+            if (!WHOLE && (!in || n >= N)) continue;
+            if constexpr (P == Up) {
+              if (g.c2) {
+                put(c2 + n, N - n, f);
+                put(c2 + N + n, N - n, u);
+              }
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                float x, da;
+                activate<T>(g.act, f[q], x, da);
+                f[q] = x * u[q];
+              }
+            } else if constexpr (P == Dh) {
+              widen<T, 8>(kept[group & 1][i - group * AHEAD][j / 2][0], u);
+              widen<T, 8>(kept[group & 1][i - group * AHEAD][j / 2][1], v);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                const float dh = f[q];
+                float x, da;
+                activate<T>(g.act, u[q], x, da);
+                f[q] = x * v[q];
+                u[q] = dh * v[q] * da;
+                v[q] = dh * x;
+              }
+              put(c2 + n, N - n, u);
+              put(c2 + g.half + n, N - n, v);
+            }
+            put(c + n, N - n, f);
           }
         }
+        if constexpr (P == Dh) asm volatile("" ::: "memory");   // this group's stores before the next loads
       }
-#pragma unroll
-      for (int i = i0; i < i0 + AHEAD; ++i) {
-        const int32_t m = now.m0 + (wm * S::MF + i) * 16 + lane % 16;
-        const bool in = m < now.rows;
-        T *c, *c2 = nullptr;
-        if constexpr (P == Dw) {
-          const tbe_stack& o = now.which == 0 ? g.o0 : now.which == 1 ? g.o1 : g.o2;
-          c = static_cast<T*>(o.data) + now.e * o.stride + m * o.ld;
-        } else {
-          c = static_cast<T*>(g.c) + m * g.ldc;
-          c2 = static_cast<T*>(g.c2) + m * g.ldc2;
-        }
-#pragma unroll
-        for (int j = 0; j < COLS; j += 2) {
-          const int32_t n = nw + j * 16;
-          float f[8];
-          eight(acc[i][j], acc[i][j + 1], f);   // (all lanes)
-          [[maybe_unused]] float u[8], v[8];
-          if constexpr (P == Up) eight(acc[i][j + HALF], acc[i][j + HALF + 1], u);
-          if (!in || n >= N) continue;
-          if constexpr (P == Up) {
-            if (g.c2) {
-              store8<T>(c2 + n, N - n, f);
-              store8<T>(c2 + N + n, N - n, u);
-            }
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              float x, da;
-              activate<T>(g.act, f[q], x, da);
-              f[q] = x * u[q];
-            }
-          } else if constexpr (P == Dh) {
-            widen<T, 8>(pu[i - i0][j / 2], u);
-            widen<T, 8>(pv[i - i0][j / 2], v);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float dh = f[q];
-              float x, da;
-              activate<T>(g.act, u[q], x, da);
-              f[q] = x * v[q];
-              u[q] = dh * v[q] * da;
-              v[q] = dh * x;
-            }
-            store8<T>(c2 + n, N - n, u);
-            store8<T>(c2 + g.half + n, N - n, v);
-          }
-          store8<T>(c + n, N - n, f);
-        }
-      }
-    }
+    };
+    // stores of 16 bytes, of which a whole tile makes as many in every wave. (Dh has
+    // waited for loads made after the fetch, and so for the fetch.)
+    constexpr int STORES = S::MF * COLS / 2 * (sizeof(T) == 4 ? 2 : 1);
+    if (whole) finish(std::true_type{});
+    else finish(std::false_type{});
+    w.later = !whole ? 0 : P == Dh ? 48 : P == Up && g.c2 ? 3 * STORES : STORES;
   }
 }
 

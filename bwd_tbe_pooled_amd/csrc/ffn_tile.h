@@ -307,12 +307,25 @@ template <typename T, class S, bool DIRECT, class A, class B>
 struct Walk {
   char* lds;
   uint32_t area = 0;   // of the next step
+  int later = 0;       // loads and stores this wave is sure to have made after the fetch of a tile's first step
   A a;
   B b;
 
+  // All but the LATER last loads and stores of every wave have been made, and its reads
+  // of LDS. (They are counted in the order in which they were issued.)
+  template <int LATER>
   __device__ __forceinline__ void arrived() const {
     typedef __attribute__((address_space(3))) char* lds_ptr;
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" :: "s"((uint32_t)(uintptr_t)(lds_ptr)lds) : "memory");
+    asm volatile("s_waitcnt vmcnt(%1) lgkmcnt(0)\n\ts_barrier"
+                 :: "s"((uint32_t)(uintptr_t)(lds_ptr)lds), "n"(LATER) : "memory");
+  }
+  // The same for a tile's first step, behind which the stores of the tile before stand.
+  __device__ __forceinline__ void first_arrived() const {
+    if (later >= 48) arrived<48>();
+    else if (later >= 24) arrived<24>();
+    else if (later >= 16) arrived<16>();
+    else if (later >= 8) arrived<8>();
+    else arrived<0>();
   }
   __device__ __forceinline__ void fetch() {
     if constexpr (DIRECT) {
@@ -338,7 +351,7 @@ struct Walk {
       if (all == 0) return next();
       Frags<S> even, odd;
       const char* now = lds + (area ^ S::AREA);
-      arrived();
+      first_arrived();
       if (1 == steps && more > 0) turn();
       if (all > 1) fetch();
       even.template read<A, B>(now, 0, row_b);
@@ -346,7 +359,7 @@ struct Walk {
       even.template mul<T>(acc);
       for (int i = 1; i < all; ++i) {
         now = lds + (area ^ S::AREA);
-        arrived();
+        arrived<0>();
         if (i + 1 == steps && more > 0) turn();
         if (i + 1 < all) fetch();
         even.template read<A, B>(now, 0, row_b);
@@ -393,92 +406,55 @@ struct Walk {
 };
 
 // The experts' rows, from the offsets: each is at least its predecessor and in
-// [0, M], whatever the memory holds. Uniform over the wave.
-struct Span {
-  int32_t e, first, end;   // expert, its rows
-  int32_t place;           // find: which of the expert's `tiles` blocks of rows times `nt`
-  int32_t tiles;
-};
+// [0, M], whatever the memory holds. In LDS, once a workgroup.
+struct Spans {
+  static constexpr int kMost = 1024;
+  int32_t first[kMost];   // of expert e; behind the last expert's
+  int32_t upto[kMost];    // blocks of rows of the experts up to e
 
-__device__ __forceinline__ int32_t wave_scan_max(int32_t x) {
+  // By every thread of the workgroup.
+  template <int BM>
+  __device__ __forceinline__ void fill(const int32_t* __restrict__ offsets, int32_t E, int32_t M) {
+    if (wave_index() == 0) {
+      int32_t low = 0, blocks = 0;
+      for (int32_t e0 = 0; e0 <= E; e0 += kWave) {
+        const int32_t e = e0 + lane_id();
+        int32_t a = e <= E ? min(max(offsets[e], 0), M) : 0;
+        int32_t z = e < E ? min(max(offsets[e + 1], 0), M) : 0;
 #pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
-    const int32_t y = __shfl_up(x, d);
-    if (lane_id() >= d) x = max(x, y);
-  }
-  return x;
-}
-__device__ __forceinline__ int32_t wave_scan_sum(int32_t x) {
+        for (int d = 1; d < kWave; d <<= 1) {
+          const int32_t y = __shfl_up(a, d);
+          if (lane_id() >= d) a = max(a, y);
+        }
+        a = max(a, low);
+        z = max(a, z);
+        int32_t n = e < E ? (z - a + BM - 1) / BM : 0;
 #pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
-    const int32_t y = __shfl_up(x, d);
-    if (lane_id() >= d) x += y;
-  }
-  return x;
-}
-
-// Blocks of BM rows of all experts.
-template <int BM>
-__device__ __forceinline__ int32_t count_blocks(const int32_t* __restrict__ offsets, int32_t E, int32_t M) {
-  int32_t all = 0, low = 0;
-  for (int32_t e0 = 0; e0 < E; e0 += kWave) {
-    const int32_t e = e0 + lane_id();
-    int32_t a = min(max(offsets[min(e, E)], 0), M);
-    int32_t z = min(max(offsets[min(e + 1, E)], 0), M);
-    a = max(wave_scan_max(a), low);
-    z = max(a, z);
-    all += (z - a + BM - 1) / BM;
-    low = __builtin_amdgcn_readlane(z, kWave - 1);
-  }
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) all += __shfl_xor(all, d);
-  return __builtin_amdgcn_readfirstlane(all);
-}
-
-// Block `tile` of the experts' rows in blocks of BM, nt of them side by side: an
-// expert's blocks are neighbours. False behind the last.
-template <int BM>
-__device__ __forceinline__ bool find_block(const int32_t* __restrict__ offsets, int32_t E, int32_t M,
-                                           int32_t nt, int32_t tile, Span& s) {
-  const int32_t want = tile / nt;
-  int32_t before = 0, low = 0;
-  for (int32_t e0 = 0; e0 < E; e0 += kWave) {
-    const int32_t e = e0 + lane_id();
-    int32_t a = min(max(offsets[min(e, E)], 0), M);
-    int32_t z = min(max(offsets[min(e + 1, E)], 0), M);
-    a = max(wave_scan_max(a), low);
-    z = max(a, z);
-    const int32_t tiles = (z - a + BM - 1) / BM;
-    const int32_t upto = before + wave_scan_sum(tiles);
-    const uint64_t hit = __ballot(upto > want);
-    if (hit) {
-      const int l = __ffsll((unsigned long long)hit) - 1;
-      s.e = e0 + l;
-      s.first = __builtin_amdgcn_readlane(a, l);
-      s.end = __builtin_amdgcn_readlane(z, l);
-      s.tiles = __builtin_amdgcn_readlane(tiles, l);
-      s.place = tile - (__builtin_amdgcn_readlane(upto, l) - s.tiles) * nt;
-      return true;
+        for (int d = 1; d < kWave; d <<= 1) {
+          const int32_t y = __shfl_up(n, d);
+          if (lane_id() >= d) n += y;
+        }
+        n += blocks;
+        if (e <= E) {
+          first[e] = a;
+          upto[e] = n;
+        }
+        low = __builtin_amdgcn_readlane(z, kWave - 1);
+        blocks = __builtin_amdgcn_readlane(n, kWave - 1);
+      }
     }
-    before = __builtin_amdgcn_readlane(upto, kWave - 1);
-    low = __builtin_amdgcn_readlane(z, kWave - 1);
+    __syncthreads();
   }
-  return false;
-}
 
-// Rows of expert e.
-__device__ __forceinline__ void expert_rows(const int32_t* __restrict__ offsets, int32_t e, int32_t M,
-                                            Span& s) {
-  int32_t low = 0;
-  for (int32_t e0 = 0; e0 <= e; e0 += kWave) {
-    const int32_t i = e0 + lane_id();
-    low = max(low, i <= e ? min(max(offsets[i], 0), M) : 0);
+  // The expert of block `want` of all experts': the first whose blocks reach behind it.
+  // Found by 64 lanes in two looks. Uniform over the wave; there is one.
+  __device__ __forceinline__ int32_t expert_of(int32_t want, int32_t E) const {
+    const int32_t step = (E + kWave - 1) / kWave;
+    const int32_t i = min((lane_id() + 1) * step, E) - 1;
+    const int32_t e0 = (__ffsll((unsigned long long)__ballot(upto[i] > want)) - 1) * step;
+    const int32_t j = min(e0 + lane_id(), E - 1);
+    return e0 + __ffsll((unsigned long long)__ballot(upto[j] > want)) - 1;
   }
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) low = max(low, __shfl_xor(low, d));
-  s.e = e;
-  s.first = __builtin_amdgcn_readfirstlane(low);
-  s.end = max(s.first, min(max(offsets[e + 1], 0), M));
-}
+};
 
 }  // namespace tbe
