@@ -66,6 +66,16 @@ __device__ __forceinline__ void store8(T* p, int32_t n, const float (&f)[8]) {
   }
 }
 template <typename T>
+__device__ __forceinline__ void store4(T* p, int32_t n, const float (&f)[4]) {
+  if (n >= 4) {
+    store_pack<T, 4>(p, narrow<T, 4>(f));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < n) p[j] = round_to<T>(f[j]);
+  }
+}
+template <typename T>
 __device__ __forceinline__ typename Pack<T, 8>::raw load8(const T* p, int32_t n) {
   typename Pack<T, 8>::raw r{};
   if (n >= 8) {
@@ -312,14 +322,145 @@ __global__ __launch_bounds__(S::NT, 2) void ffn_kernel(Args g) {
   }
 }
 
+// Few rows an expert (decoding): what counts is that the weights are read once, at
+// memory's rate. A workgroup has 16 columns of an expert's products (NB = 2: of Up both
+// products', of Down 32) and up to 16 MB of its rows at a time; its waves share k. A
+// lane's pieces of a matrix row go straight to registers, and the waves' sums meet in
+// LDS. WAVES: 4, or 16 where the workgroups are too few to fill the card.
+template <typename T, Product P, int MB, int NB, int WAVES>
+__global__ __launch_bounds__(WAVES * kWave) void ffn_few_kernel(Args g) {
+  constexpr int VE = 16 / (int)sizeof(T);
+  constexpr int BK = 8 * VE;   // of k in one turn of a wave: a line of 128 bytes, in two halves
+  constexpr int COLS = P == Up ? 16 : NB * 16;
+  static_assert(P == Down || NB == 2, "both products of Up");
+  __shared__ f32x4 meet[WAVES][MB][NB][kWave];
+  const int wave = wave_index(), lane = lane_id();
+  const int32_t e = blockIdx.x / g.nt, n0 = (int32_t)(blockIdx.x % g.nt) * COLS;
+  const int32_t first = first_row(g.offsets, e, g.M);
+  const int32_t end = max(first, min(max(g.offsets[e + 1], 0), g.M));
+  const int32_t K = P == Up ? g.D : g.F, N = P == Up ? g.F : g.D;
+  const int kl = lane / 16 * VE;   // of k, in half a line: this lane's
+  const T* rows_b[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const tbe_stack& m = P == Up && j ? g.b1 : g.b0;
+    const int32_t n = n0 + lane % 16 + (P == Up ? 0 : j * 16);
+    rows_b[j] = matrix<T>(m, e) + min(n, N - 1) * m.ld + kl;
+  }
+  for (int32_t m0 = first; m0 < end; m0 += 16 * MB) {
+    const T* rows_a[MB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+      rows_a[i] = static_cast<const T*>(g.a) + (int64_t)min(m0 + i * 16 + lane % 16, end - 1) * g.lda + kl;
+    f32x4 acc[MB][NB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // COUNT turns from k, their loads in flight together; WHOLE: all of them in the rows
+    auto turns = [&](int32_t k, auto count, auto is_whole) {
+      constexpr int COUNT = decltype(count)::value;
+      auto piece = [&](const T* row, int32_t at) {   // 16 bytes, zeros behind K
+        if constexpr (decltype(is_whole)::value) return __builtin_bit_cast(uint4, load_pack<T, VE>(row + at));
+        const int32_t n = K - at - kl;
+        uint4 r = make_uint4(0, 0, 0, 0);
+        if (n >= VE) {
+          r = __builtin_bit_cast(uint4, load_pack<T, VE>(row + at));
+        } else if (n > 0) {
+          T x[VE];
+#pragma unroll
+          for (int j = 0; j < VE; ++j) x[j] = j < n ? row[at + j] : T{};
+          r = __builtin_bit_cast(uint4, x);
+        }
+        return r;
+      };
+      uint4 a[COUNT][MB][2], b[COUNT][NB][2];
+#pragma unroll
+      for (int t = 0; t < COUNT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int32_t at = k + t * WAVES * BK + h * BK / 2;
+#pragma unroll
+          for (int j = 0; j < NB; ++j) b[t][j][h] = piece(rows_b[j], at);
+#pragma unroll
+          for (int i = 0; i < MB; ++i) a[t][i][h] = piece(rows_a[i], at);
+        }
+#pragma unroll
+      for (int t = 0; t < COUNT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j) acc[i][j] = Mma<T>::mul(b[t][j][h], a[t][i][h], acc[i][j]);
+    };
+    int32_t k = wave * BK;
+    constexpr int TURNS = MB == 1 ? 4 : 2;
+    for (; k + ((TURNS - 1) * WAVES + 1) * BK <= K; k += TURNS * WAVES * BK)
+      turns(k, std::integral_constant<int, TURNS>{}, std::true_type{});
+    for (; k < K; k += WAVES * BK) turns(k, std::integral_constant<int, 1>{}, std::false_type{});
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) meet[wave][i][j][lane] = acc[i][j];
+    __syncthreads();
+    for (int i = wave; i < MB; i += WAVES) {   // a block of 16 rows' sums
+      f32x4 s[NB];
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        s[j] = meet[0][i][j][lane];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) s[j] += meet[w][i][j][lane];
+      }
+      const int32_t m = m0 + i * 16 + lane % 16;
+      if (m >= end) continue;
+      T* c = static_cast<T*>(g.c) + m * g.ldc;
+      if constexpr (P == Up) {
+        const int32_t n = n0 + lane / 16 * 4;
+        float f[4], u[4], h[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float da;
+          f[q] = s[0][q];
+          u[q] = s[1][q];
+          activate<T>(g.act, f[q], h[q], da);
+          h[q] *= u[q];
+        }
+        if (g.c2) {
+          T* c2 = static_cast<T*>(g.c2) + m * g.ldc2;
+          store4<T>(c2 + n, N - n, f);
+          store4<T>(c2 + N + n, N - n, u);
+        }
+        store4<T>(c + n, N - n, h);
+      } else {
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          const int32_t n = n0 + j * 16 + lane / 16 * 4;
+          const float f[4] = {s[j][0], s[j][1], s[j][2], s[j][3]};
+          store4<T>(c + n, N - n, f);
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
 int64_t blocks_of(int64_t n, int64_t b) { return (n + b - 1) / b; }
+
+// Tiles of shape S that have work, at least.
+template <Product P, class S>
+int64_t tiles_of(const Args& g) {
+  if (P == Dw)
+    return (int64_t)g.E * (2 * blocks_of(g.F, S::BM) * blocks_of(g.D, S::BN) + blocks_of(g.D, S::BM) * blocks_of(g.F, S::BN));
+  return std::max<int64_t>(std::min(g.E, g.M), blocks_of(g.M, S::BM)) *
+         blocks_of(P == Up || P == Dh ? g.F : g.D, P == Up ? S::BN / 2 : S::BN);
+}
 
 // Launches one product with tiles of shape S.
 template <typename T, Product P, class S>
 hipError_t launch(Args g, bool direct, hipStream_t s) {
   if constexpr (P == Dw) {
-    g.tiles = (int64_t)g.E * (2 * blocks_of(g.F, S::BM) * blocks_of(g.D, S::BN) +
-                              blocks_of(g.D, S::BM) * blocks_of(g.F, S::BN));
+    g.tiles = tiles_of<P, S>(g);
   } else {
     constexpr int BN = P == Up ? S::BN / 2 : S::BN;
     g.nt = (int32_t)blocks_of(P == Up || P == Dh ? g.F : g.D, BN);
@@ -327,7 +468,7 @@ hipError_t launch(Args g, bool direct, hipStream_t s) {
     g.tiles = (g.M / S::BM + std::min(g.E, g.M)) * (int64_t)g.nt;
   }
   // as many workgroups as find room at once, a multiple of the XCDs
-  constexpr int64_t kRoom = 256 * (2 * S::AREA > (80 << 10) ? 1 : 2);
+  constexpr int64_t kRoom = 256 * (S::BM * S::BN >= 65536 ? 1 : S::BM * S::BN >= 16384 ? 2 : 4);
   const unsigned grid = (unsigned)std::min(xcd_grid(g.tiles), kRoom);
   if (direct) ffn_kernel<T, P, S, true><<<grid, S::NT, 0, s>>>(g);
   else if constexpr (S::NT == 256) ffn_kernel<T, P, S, false><<<grid, S::NT, 0, s>>>(g);
@@ -348,14 +489,48 @@ struct Aligned {
   }
 };
 
-using Middle = Shape<2, 2, 4, 4>;   // 128 x 128
-using Large = Shape<2, 4, 8, 4>;    // 256 x 256
+using Small = Shape<4, 1, 1, 4>;    // 64 x 64, four workgroups on a CU
+using Middle = Shape<2, 2, 4, 4>;   // 128 x 128, two
+using Large = Shape<2, 4, 8, 4>;    // 256 x 256, one
 
-// Launches one product with the tiles that suit it.
+template <typename T, Product P, int MB>
+hipError_t launch_few(Args g, hipStream_t s) {
+  // workgroups that have work, at most: 512 give every CU eight waves
+  constexpr int WIDE = P == Up ? 16 : 32;
+  const int32_t cols = P == Up ? g.F : g.D;
+  if (std::min(g.E, g.M) * blocks_of(cols, WIDE) >= 512) {
+    g.nt = (int32_t)blocks_of(cols, WIDE);
+    ffn_few_kernel<T, P, MB, 2, 4><<<(unsigned)(g.E * g.nt), 4 * kWave, 0, s>>>(g);
+  } else {
+    constexpr int WAVES = 16 / MB;
+    g.nt = (int32_t)blocks_of(cols, 16);
+    ffn_few_kernel<T, P, MB, P == Up ? 2 : 1, WAVES><<<(unsigned)(g.E * g.nt), WAVES * kWave, 0, s>>>(g);
+  }
+  return hipGetLastError();
+}
+
+// Launches one product with the tiles that suit it: the largest of which every CU has
+// one, and an expert's rows fill most of (256 rows an expert and 64 experts of 2048 x
+// 768: Large 217 us forward, Middle 209 for 192). With less than one Middle tile a CU
+// Small is faster (one expert of 4096 x 8192, 192 rows: 153 against 171 us). Few rows
+// are bound by the weights: where Middle has few tiles, ffn_few has more workgroups
+// (the same, 1 row: 47 against 144 us; 63 rows: 101 against 144; eight experts of 4096
+// x 1536: 62 against 87 for 1 row, 85 against 88 for 31, 127 against 89 for 63), else
+// Middle's tiles read them as fast (64 experts: 131 and 131 us for 1 row, 160 and 127
+// for 15).
 template <typename T, Product P>
 hipError_t launch_product(const Args& g, bool direct, hipStream_t s) {
+  const int64_t rows = g.M / g.E, tiles = tiles_of<P, Middle>(g);
+  if constexpr (P == Up || P == Down) {
+    if (tiles < 512) {
+      if (rows < 16) return launch_few<T, P, 1>(g, s);
+      if (rows < 32) return launch_few<T, P, 2>(g, s);
+      if (rows < 64 && tiles <= 128) return launch_few<T, P, 4>(g, s);
+    }
+  }
+  if (tiles < 256) return launch<T, P, Small>(g, direct, s);
   if constexpr (sizeof(T) == 2)
-    if (direct && g.M / g.E >= 256) return launch<T, P, Large>(g, direct, s);
+    if (direct && rows >= 256 && tiles_of<P, Large>(g) >= 256) return launch<T, P, Large>(g, direct, s);
   return launch<T, P, Middle>(g, direct, s);
 }
 

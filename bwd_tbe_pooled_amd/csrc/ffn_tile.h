@@ -457,4 +457,13 @@ struct Spans {
   }
 };
 
+// First row of expert e, as Spans has it, by one wave.
+__device__ __forceinline__ int32_t first_row(const int32_t* __restrict__ offsets, int32_t e, int32_t M) {
+  int32_t x = 0;
+  for (int32_t i = lane_id(); i <= e; i += kWave) x = max(x, offsets[i]);
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) x = max(x, __shfl_xor(x, d));
+  return min(__builtin_amdgcn_readfirstlane(x), M);
+}
+
 }  // namespace tbe
