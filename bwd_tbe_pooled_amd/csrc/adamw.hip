@@ -19,9 +19,7 @@ namespace tbe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 4096;      // elements of a workgroup: whole blocks of the 8-bit moments
 constexpr int kTensors = 52;      // of a launch: the arguments stay within 4 KiB
-static_assert(kChunk % kAdamBlock == 0, "chunks of whole blocks");
 
 struct Args {
   const int64_t* step;
@@ -44,15 +42,19 @@ __device__ __forceinline__ double power(double b, uint64_t t) {
   return r;
 }
 
-// Largest over the lanes that hold a block.
+// Largest over the LANES neighbouring lanes that hold a block, all of them active.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xf, 0xf, false);
+}
 template <int LANES>
-__device__ __forceinline__ float block_max(float x) {
-  x = fmaxf(x, dpp_f32<0xB1>(x));
-  x = fmaxf(x, dpp_f32<0x4E>(x));
-  x = fmaxf(x, dpp_f32<0x141>(x));
-  x = fmaxf(x, dpp_f32<0x140>(x));
-  x = fmaxf(x, __shfl_xor(x, 16));
-  if constexpr (LANES == 64) x = fmaxf(x, __shfl_xor(x, 32));
+__device__ __forceinline__ uint32_t block_max(uint32_t x) {
+  x = max(x, dpp_u32<0xB1>(x));
+  x = max(x, dpp_u32<0x4E>(x));
+  x = max(x, dpp_u32<0x141>(x));
+  x = max(x, dpp_u32<0x140>(x));
+  x = max(x, (uint32_t)__shfl_xor((int)x, 16));
+  if constexpr (LANES == 64) x = max(x, (uint32_t)__shfl_xor((int)x, 32));
   return x;
 }
 
@@ -74,35 +76,51 @@ __device__ __forceinline__ void decode(const Codes<V>& q, float scale, float (&f
   }
 }
 
-// f as codes and their block's scale. Rounded to nearest even, at most half a
-// step (2^-4 of the value) off; LEAST holds what is above zero at 2^-9, the
-// smallest code, at least. Elements from `n` on are none.
-template <int V, bool LEAST>
-__device__ __forceinline__ Codes<V> encode(float (&f)[V], int n, float* scale) {
-  constexpr float kInf = __builtin_inff();
-  float top = 0.f;
+// Codes of f * inv; LEAST holds what is above zero at 2^-9, the smallest code, at least.
+// What is not finite becomes NaN (only asked of blocks that hold such a value).
+template <int V, bool LEAST, bool FINITE>
+__device__ __forceinline__ Codes<V> codes_of(const float (&f)[V], float inv) {
+  float q[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const float a = fabsf(f[j]);
-    top = fmaxf(top, j < n && a < kInf ? a : 0.f);
-  }
-  top = block_max<kAdamBlock / V>(top);
-  const bool some = top >= 0x1p-100f;
-  const float inv = some ? 448.f / top : 0.f;
-  *scale = some ? top * (1.f / 448.f) : 0.f;
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    float q = f[j] * inv;
-    if (LEAST) q = f[j] > 0.f && some ? fmaxf(q, 0x1p-9f) : q;
-    f[j] = fabsf(f[j]) < kInf ? q : __builtin_nanf("");
+    q[j] = f[j] * inv;
+    if (LEAST) q[j] = f[j] > 0.f && inv > 0.f ? fmaxf(q[j], 0x1p-9f) : q[j];
+    if (!FINITE) q[j] = fabsf(f[j]) < __builtin_inff() ? q[j] : __builtin_nanf("");
   }
   Codes<V> r;
 #pragma unroll
   for (int i = 0; i < V / 4; ++i) {
-    int w = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i], f[4 * i + 1], 0, false);
-    r.w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i + 2], f[4 * i + 3], w, true);
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i], q[4 * i + 1], 0, false);
+    r.w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i + 2], q[4 * i + 3], w, true);
   }
   return r;
+}
+
+// f as codes and their block's scale. Rounded to nearest even, at most half a step (2^-4
+// of the value) off. Elements that do not exist are zeros. The largest magnitude is found
+// on the bit patterns, where infinities and NaN are above all numbers: then it is looked
+// for again among the finite ones.
+template <int V, bool LEAST>
+__device__ __forceinline__ Codes<V> encode(const float (&f)[V], float* scale) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < V; ++j) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
+  top = block_max<kAdamBlock / V>(top);
+  const bool finite = top < 0x7f800000u;
+  if (!finite) {
+    top = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const uint32_t u = __float_as_uint(f[j]) & 0x7fffffffu;
+      top = max(top, u < 0x7f800000u ? u : 0u);
+    }
+    top = block_max<kAdamBlock / V>(top);
+  }
+  const float t = __uint_as_float(top);
+  const bool some = t >= 0x1p-100f;
+  const float inv = some ? 448.f / t : 0.f;
+  *scale = some ? t * (1.f / 448.f) : 0.f;
+  return finite ? codes_of<V, LEAST, true>(f, inv) : codes_of<V, LEAST, false>(f, inv);
 }
 
 // V elements from p + at, of which n exist (all of them in whole vectors).
@@ -118,20 +136,32 @@ __device__ __forceinline__ void store_some(T* p, int n, const float (&f)[V]) {
     if (j < n) p[j] = round_to<T>(f[j]);
 }
 
-// P, G, C: types of parameters, gradients and copies (C = void: none).
-template <typename P, typename G, typename C, int BITS>
+// Elements of a thread's vector, and vectors of a thread where there is much to do: what
+// is in flight covers memory's latency (357 million float32 parameters: 1759 us with 4
+// vectors of 4, 1806 with 2; 738 million of 16 bits with 8-bit moments: 1339 with 2
+// vectors of 8, 1299 with 1). With little to do more workgroups are faster, and one
+// vector is taken.
+template <typename P>
+constexpr int vector_of() { return sizeof(P) == 4 ? 4 : 8; }
+template <typename P, int BITS>
+constexpr int most_vectors() { return (BITS == 32 ? 16 : 8) / vector_of<P>(); }
+constexpr int64_t kMuch = int64_t(1) << 22;   // elements
+
+// P, G, C: types of parameters, gradients and copies (C = void: none). U: vectors of a
+// thread.
+template <typename P, typename G, typename C, int BITS, int U>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(Args a) {
   constexpr bool kCopy = !__is_same(C, void);
   using CT = std::conditional_t<kCopy, C, bf16_t>;
-  constexpr int V = sizeof(P) == 4 ? 4 : 8;
-  constexpr int U = kChunk / (kThreads * V);   // vectors of a thread
-  // the tensor: the first whose end is behind this chunk
-  int lo = 0, hi = a.count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if ((int)blockIdx.x < a.end[mid]) hi = mid;
-    else lo = mid + 1;
-  }
+  constexpr int V = vector_of<P>();
+  constexpr int kChunk = kThreads * V * U;
+  static_assert(kChunk % kAdamBlock == 0, "chunks of whole blocks");
+  const int64_t step = *a.step;
+  const float lr = *a.lr;
+  const float scale = a.scale ? *a.scale : 1.f;
+  // the tensor: the first whose end is behind this chunk; a lane looks at each end
+  const int lane = lane_id();
+  const int lo = __popcll(__ballot(lane < a.count && a.end[lane < kTensors ? lane : 0] <= (int)blockIdx.x));
   const tbe_adamw_tensor& t = a.t[lo];
   const int64_t base = (int64_t)((int)blockIdx.x - (lo ? a.end[lo - 1] : 0)) * kChunk;
   P* const p = static_cast<P*>(t.p) + base;
@@ -168,10 +198,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Args a) {
       sv[u] = t.vscale[block0 + i / kAdamBlock];
     }
   }
-  const int64_t step = *a.step;
   const uint64_t n_step = step < 1 ? 1 : (uint64_t)step;
-  const float lr = *a.lr;
-  const float scale = a.scale ? *a.scale : 1.f;
   const float b1 = (float)a.beta1, b2 = (float)a.beta2;
   const float g1 = (float)(1.0 - a.beta1), g2 = (float)(1.0 - a.beta2);
   const float move = (float)((double)lr / (1.0 - power(a.beta1, n_step)));
@@ -217,9 +244,9 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Args a) {
       m[u][j] = fmaf(b1, m[u][j], g1 * gj);
       const float old = BITS == 32 ? v[u][j] : v[u][j] * v[u][j];
       const float vn = fmaf(b2, old, g2 * gj * gj);
-      const float root = sqrtf(vn);
+      const float root = __builtin_amdgcn_sqrtf(vn);   // (1 ulp, as the reciprocal)
       v[u][j] = BITS == 32 ? vn : root;
-      x[u][j] = fmaf(keep, x[u][j], -(move * m[u][j]) / fmaf(root, unbias, a.eps));
+      x[u][j] = fmaf(-(move * m[u][j]), __builtin_amdgcn_rcpf(fmaf(root, unbias, a.eps)), keep * x[u][j]);
     }
     if (n == V) {
       store_pack_once<P, V>(p + i, narrow<P, V>(x[u]));
@@ -238,7 +265,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Args a) {
     }
     if constexpr (BITS == 8) {   // every lane of a block takes part in its reduction
       float ms, vs;
-      const Codes<V> em = encode<V, false>(m[u], n, &ms), ev = encode<V, true>(v[u], n, &vs);
+      const Codes<V> em = encode<V, false>(m[u], &ms), ev = encode<V, true>(v[u], &vs);
       if (n == V) {
         *reinterpret_cast<Codes<V>*>(m8 + i) = em;
         *reinterpret_cast<Codes<V>*>(v8 + i) = ev;
@@ -290,14 +317,24 @@ hipError_t launch_adamw(const tbe_adamw_desc& d, const tbe_adamw_tensor* tensors
   a.decay = (float)d.weight_decay;
   a.count = 0;
   int64_t blocks = 0;
+  int64_t elements = 0;
+  for (int64_t i = 0; i < count; ++i) elements += tensors[i].n;
+  const bool much = elements >= kMuch;
+  const int vector = d.pdtype == TBE_F32 ? 4 : 8, most = (d.bits == 32 ? 16 : 8) / vector;
+  const int64_t chunk = (int64_t)kThreads * vector * (much ? most : 1);
   auto flush = [&]() -> hipError_t {
     if (a.count == 0) return hipSuccess;
     const hipError_t e = with_types(d, [&](auto* p, auto* g, auto* c) {
       using P = std::remove_pointer_t<decltype(p)>;
       using G = std::remove_pointer_t<decltype(g)>;
       using C = std::remove_pointer_t<decltype(c)>;
-      if (d.bits == 32) adamw_kernel<P, G, C, 32><<<(unsigned)blocks, kThreads, 0, s>>>(a);
-      else adamw_kernel<P, G, C, 8><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+      auto run = [&](auto bits) {
+        constexpr int BITS = decltype(bits)::value, MOST = most_vectors<P, BITS>();
+        if (much) adamw_kernel<P, G, C, BITS, MOST><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+        else adamw_kernel<P, G, C, BITS, 1><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+      };
+      if (d.bits == 32) run(std::integral_constant<int, 32>{});
+      else run(std::integral_constant<int, 8>{});
       return hipGetLastError();
     });
     a.count = 0;
@@ -307,9 +344,9 @@ hipError_t launch_adamw(const tbe_adamw_desc& d, const tbe_adamw_tensor* tensors
   for (int64_t i = 0; i < count; ++i) {
     tbe_adamw_tensor t = tensors[i];
     while (t.n > 0) {   // a tensor of more workgroups than a launch has left is cut
-      const int64_t need = (t.n + kChunk - 1) / kChunk;
+      const int64_t need = (t.n + chunk - 1) / chunk;
       const int64_t take = std::min(need, kMaxBlocks - blocks);
-      const int64_t elems = std::min(t.n, take * kChunk);
+      const int64_t elems = std::min(t.n, take * chunk);
       tbe_adamw_tensor part = t;
       part.n = elems;
       a.t[a.count] = part;

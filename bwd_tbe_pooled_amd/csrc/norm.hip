@@ -395,11 +395,11 @@ __global__ __launch_bounds__(kThreads) void norm_join_kernel(const float* parts,
   else static_cast<bf16_t*>(out)[d] = round_to<bf16_t>(v);
 }
 
-// Calls f(VE, LPR, NV) with the shape for rows of D columns. The forward takes
-// two vectors a lane where one wave then holds the row; the backward, with five
-// values a column, one vector as long as 1024 lanes hold the row.
-template <typename T, bool TWO, typename F>
-bool with_shape(int32_t D, bool two, F f) {
+// Calls f(VE, LPR, NV) with the shape for rows of D columns: one vector a lane as long
+// as 1024 lanes hold the row. (Two vectors on half the lanes hold fewer waves on a CU:
+// 16384 rows of 4096 bf16, forward and backward, 131 us against 126.)
+template <typename T, typename F>
+bool with_shape(int32_t D, F f) {
   constexpr int VE = pack_elems<T>();
   const int64_t v = ((int64_t)D + VE - 1) / VE;
   auto shape = [&](auto ve, auto lpr, auto nv) { f(ve, lpr, nv); };
@@ -410,17 +410,12 @@ bool with_shape(int32_t D, bool two, F f) {
   else if (v <= 16) TBE_SHAPE(VE, 16, 1);
   else if (v <= 32) TBE_SHAPE(VE, 32, 1);
   else if (v <= 64) TBE_SHAPE(VE, 64, 1);
-  else if (v <= kMaxVectors) {
-    if constexpr (TWO) {
-      if (two && v > 64 && v <= 128) return TBE_SHAPE(VE, 64, 2), true;
-      if (two && v > 256 && v <= 512) return TBE_SHAPE(VE, 256, 2), true;
-    }
-    if (v <= 128) TBE_SHAPE(VE, 128, 1);
-    else if (v <= 256) TBE_SHAPE(VE, 256, 1);
-    else if (v <= 512) TBE_SHAPE(VE, 512, 1);
-    else if (v <= 1024) TBE_SHAPE(VE, 1024, 1);
-    else TBE_SHAPE(VE, 1024, 2);
-  } else return false;
+  else if (v <= 128) TBE_SHAPE(VE, 128, 1);
+  else if (v <= 256) TBE_SHAPE(VE, 256, 1);
+  else if (v <= 512) TBE_SHAPE(VE, 512, 1);
+  else if (v <= 1024) TBE_SHAPE(VE, 1024, 1);
+  else if (v <= kMaxVectors) TBE_SHAPE(VE, 1024, 2);
+  else return false;
 #undef TBE_SHAPE
   return true;
 }
@@ -440,10 +435,11 @@ hipError_t launch_norm_forward(const tbe_norm_desc& d, const void* x, int64_t ld
                          (float)(1.0 / d.D)};
   return with_type(d.dtype, [&](auto t) {
     using T = decltype(t);
-    const bool done = with_shape<T, true>(d.D, d.N > 1024, [&](auto ve, auto lpr, auto nv) {
+    const bool done = with_shape<T>(d.D, [&](auto ve, auto lpr, auto nv) {
       constexpr int LPR = decltype(lpr)::value;
       constexpr int THREADS = LPR > 256 ? LPR : 256;
       const int64_t rows = THREADS / LPR;
+      // as many as find room at once, eight waves on a SIMD
       const int64_t blocks = std::min<int64_t>((d.N + rows - 1) / rows, 2048 / (THREADS / 256));
       norm_forward_kernel<T, decltype(ve)::value, LPR, decltype(nv)::value, THREADS>
           <<<(unsigned)blocks, THREADS, 0, s>>>(a);
@@ -465,7 +461,7 @@ hipError_t launch_norm_backward(const tbe_norm_desc& d, const void* dy, int64_t 
   if (d.N > 0) {
     e = with_type(d.dtype, [&](auto t) {
       using T = decltype(t);
-      const bool done = with_shape<T, false>(d.D, false, [&](auto ve, auto lpr, auto nv) {
+      const bool done = with_shape<T>(d.D, [&](auto ve, auto lpr, auto nv) {
         constexpr int LPR = decltype(lpr)::value;
         const int64_t rows = kThreads / LPR;
         P = (int32_t)std::min<int64_t>(norm_partials(d), (d.N + rows - 1) / rows);
