@@ -219,44 +219,59 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(BackwardArgs a)
   if (n < a.N) load(n);
   for (int64_t n0 = (int64_t)blockIdx.x * kRows; n0 < a.N; n0 += step, n += step) {
     const bool live = n < a.N;
-    float x[NV][VE], g[NV][VE];
+    // the row stays as it was loaded: widened twice, it takes half the registers
+    typename Pack<T, VE>::raw x[NV], g[NV];
     const float mean = live ? st.x : 0.f;
     const float r = live ? st.y : 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (live && c.col[i] >= 0) {
-        widen<T, VE>(rx[i], x[i]);
-        widen<T, VE>(rg[i], g[i]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < VE; ++j) x[i][j] = mean, g[i][j] = 0.f;
-      }
+      x[i] = rx[i];
+      g[i] = rg[i];
+      if (!live || c.col[i] < 0) zero_raw(x[i]), zero_raw(g[i]);
     }
     if (n + step < a.N) load(n + step);
     float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      float fx[VE], fg[VE];
+      widen<T, VE>(x[i], fx);
+      widen<T, VE>(g[i], fg);
 #pragma unroll
       for (int j = 0; j < VE; ++j) {
-        x[i][j] -= mean;
-        const float v = j >= c.skip[i] ? g[i][j] * w[i][j] : 0.f;
+        const bool own = j >= c.skip[i];   // (none of a vector that does not exist)
+        const float u = own ? fx[j] - mean : 0.f;
+        const float v = own ? fg[j] * w[i][j] : 0.f;
         s[0] += v;
-        s[1] = fmaf(v, x[i][j], s[1]);
-        s[2] += j >= c.skip[i] ? x[i][j] : 0.f;
+        s[1] = fmaf(v, u, s[1]);
+        s[2] += u;
       }
+    }
     row_sums<LPR, 3>(s, lds, turn);
     const float lost = s[2] * a.inv_d;
     const float m0 = s[0] * a.inv_d;
     const float m1 = fmaf(-lost, s[0], s[1]) * r * a.inv_d;
+    if constexpr (NV > 1 && VE == 8) {   // (the compiler would keep the widened row)
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t p = x[i][k], q = g[i][k];
+          asm volatile("" : "+v"(p), "+v"(q));
+          x[i][k] = p;
+          g[i][k] = q;
+        }
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float o[VE];
+      float fx[VE], fg[VE], o[VE];
+      widen<T, VE>(x[i], fx);
+      widen<T, VE>(g[i], fg);
 #pragma unroll
       for (int j = 0; j < VE; ++j) {
-        const float xh = (x[i][j] - lost) * r;
-        o[j] = r * (fmaf(g[i][j], w[i][j], -m0) - xh * m1);
-        dw[i][j] = fmaf(g[i][j], xh, dw[i][j]);
-        db[i][j] += g[i][j];
+        const float xh = (fx[j] - mean - lost) * r;
+        o[j] = r * (fmaf(fg[j], w[i][j], -m0) - xh * m1);
+        dw[i][j] = fmaf(fg[j], xh, dw[i][j]);
+        db[i][j] += fg[j];
       }
       if (live && c.col[i] >= 0)
         store_pack_once<T, VE>(static_cast<T*>(a.dx) + n * a.lddx + c.col[i], narrow<T, VE>(o));
@@ -291,33 +306,63 @@ __global__ __launch_bounds__(kThreads) void norm_backward_kernel(BackwardArgs a)
   }
 }
 
-// Rows wider than the registers hold: a workgroup reads its row for each pass.
+// Rows wider than the registers hold: a workgroup reads its row for each pass, vector
+// by vector. f(column, first of its own elements) for each vector of the lane.
+template <int VE, typename F>
+__device__ __forceinline__ void each_vector(int32_t D, F f) {
+  const int32_t vectors = (int32_t)(((int64_t)D + VE - 1) / VE);
+  for (int32_t v = threadIdx.x; v < vectors; v += kThreads) f(pack_column<VE>(v, D), pack_overlap<VE>(v, D));
+}
+template <int VE>
+__device__ __forceinline__ void load_or(const void* p, int32_t type, int32_t at, float other, float (&f)[VE]) {
+  if (p) {
+    load_as<VE>(p, type, at, f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VE; ++j) f[j] = other;
+  }
+}
+
 template <typename T>
 __global__ __launch_bounds__(kThreads) void norm_wide_forward_kernel(ForwardArgs a) {
+  constexpr int VE = pack_elems<T>();
   __shared__ float lds[2][kThreads / kWave][2];
   int turn = 0;
   for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + n * a.ldx;
     T* y = static_cast<T*>(a.y) + n * a.ldy;
     float s[2] = {0.f, 0.f};
-    for (int32_t d = threadIdx.x; d < a.D; d += kThreads) s[0] += to_float(x[d]);
+    each_vector<VE>(a.D, [&](int32_t at, int32_t own) {
+      float f[VE];
+      widen<T, VE>(load_pack<T, VE>(x + at), f);
+#pragma unroll
+      for (int j = 0; j < VE; ++j) s[0] += j >= own ? f[j] : 0.f;
+    });
     row_sums<kThreads, 2>(s, lds, turn);
     const float mean = s[0] * a.inv_d;
     s[0] = s[1] = 0.f;
-    for (int32_t d = threadIdx.x; d < a.D; d += kThreads) {
-      const float v = to_float(x[d]) - mean;
-      s[0] += v;
-      s[1] = fmaf(v, v, s[1]);
-    }
+    each_vector<VE>(a.D, [&](int32_t at, int32_t own) {
+      float f[VE];
+      widen<T, VE>(load_pack<T, VE>(x + at), f);
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        const float v = j >= own ? f[j] - mean : 0.f;
+        s[0] += v;
+        s[1] = fmaf(v, v, s[1]);
+      }
+    });
     row_sums<kThreads, 2>(s, lds, turn);
     const float lost = s[0] * a.inv_d;
     const float r = 1.f / sqrtf(fmaxf(fmaf(-lost, lost, s[1] * a.inv_d), 0.f) + a.eps);
-    for (int32_t d = threadIdx.x; d < a.D; d += kThreads) {
-      float w[1] = {1.f}, b[1] = {0.f};
-      if (a.w) load_as<1>(a.w, a.wtype, d, w);
-      if (a.b) load_as<1>(a.b, a.wtype, d, b);
-      y[d] = round_to<T>(fmaf((to_float(x[d]) - mean - lost) * r, w[0], b[0]));
-    }
+    each_vector<VE>(a.D, [&](int32_t at, int32_t) {
+      float f[VE], w[VE], b[VE];
+      widen<T, VE>(load_pack<T, VE>(x + at), f);
+      load_or<VE>(a.w, a.wtype, at, 1.f, w);
+      load_or<VE>(a.b, a.wtype, at, 0.f, b);
+#pragma unroll
+      for (int j = 0; j < VE; ++j) f[j] = fmaf((f[j] - mean - lost) * r, w[j], b[j]);
+      store_pack_once<T, VE>(y + at, narrow<T, VE>(f));
+    });
     if (threadIdx.x == 0) {
       a.stats[2 * n] = mean + lost;
       a.stats[2 * n + 1] = r;
@@ -328,6 +373,7 @@ __global__ __launch_bounds__(kThreads) void norm_wide_forward_kernel(ForwardArgs
 // A workgroup's partial rows are in memory; a column is always its lane's.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void norm_wide_backward_kernel(BackwardArgs a) {
+  constexpr int VE = pack_elems<T>();
   __shared__ float lds[2][kThreads / kWave][3];
   int turn = 0;
   float* dw = a.parts + (int64_t)blockIdx.x * 2 * a.D;
@@ -338,30 +384,62 @@ __global__ __launch_bounds__(kThreads) void norm_wide_backward_kernel(BackwardAr
     T* dx = static_cast<T*>(a.dx) + n * a.lddx;
     const float mean = a.stats[2 * n], r = a.stats[2 * n + 1];
     float s[3] = {0.f, 0.f, 0.f};
-    for (int32_t d = threadIdx.x; d < a.D; d += kThreads) {
-      float w[1] = {1.f};
-      if (a.w) load_as<1>(a.w, a.wtype, d, w);
-      const float v = to_float(g[d]) * w[0], u = to_float(x[d]) - mean;
-      s[0] += v;
-      s[1] = fmaf(v, u, s[1]);
-      s[2] += u;
-    }
+    each_vector<VE>(a.D, [&](int32_t at, int32_t own) {
+      float fx[VE], fg[VE], w[VE];
+      widen<T, VE>(load_pack<T, VE>(x + at), fx);
+      widen<T, VE>(load_pack<T, VE>(g + at), fg);
+      load_or<VE>(a.w, a.wtype, at, 1.f, w);
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        const float u = j >= own ? fx[j] - mean : 0.f, v = j >= own ? fg[j] * w[j] : 0.f;
+        s[0] += v;
+        s[1] = fmaf(v, u, s[1]);
+        s[2] += u;
+      }
+    });
     row_sums<kThreads, 3>(s, lds, turn);
     const float lost = s[2] * a.inv_d;
     const float m0 = s[0] * a.inv_d;
     const float m1 = fmaf(-lost, s[0], s[1]) * r * a.inv_d;
-    for (int32_t d = threadIdx.x; d < a.D; d += kThreads) {
-      float w[1] = {1.f};
-      if (a.w) load_as<1>(a.w, a.wtype, d, w);
-      const float gd = to_float(g[d]);
-      const float xh = (to_float(x[d]) - mean - lost) * r;
-      dx[d] = round_to<T>(r * (fmaf(gd, w[0], -m0) - xh * m1));
-      if (a.sums) {
-        const bool first = n == blockIdx.x;
-        dw[d] = fmaf(gd, xh, first ? 0.f : dw[d]);
-        db[d] = gd + (first ? 0.f : db[d]);
+    each_vector<VE>(a.D, [&](int32_t at, int32_t own) {
+      float fx[VE], fg[VE], w[VE], o[VE];
+      widen<T, VE>(load_pack<T, VE>(x + at), fx);
+      widen<T, VE>(load_pack<T, VE>(g + at), fg);
+      load_or<VE>(a.w, a.wtype, at, 1.f, w);
+      const bool first = n == blockIdx.x;
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        const float xh = (fx[j] - mean - lost) * r;
+        o[j] = r * (fmaf(fg[j], w[j], -m0) - xh * m1);
+        fx[j] = xh;
       }
-    }
+      store_pack_once<T, VE>(dx + at, narrow<T, VE>(o));
+      if (!a.sums) return;
+      if (own == 0) {
+        float pw[VE], pb[VE];
+        if (first) {
+#pragma unroll
+          for (int j = 0; j < VE; ++j) pw[j] = pb[j] = 0.f;
+        } else {
+          widen<float, VE>(load_pack<float, VE>(dw + at), pw);
+          widen<float, VE>(load_pack<float, VE>(db + at), pb);
+        }
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          pw[j] = fmaf(fg[j], fx[j], pw[j]);
+          pb[j] += fg[j];
+        }
+        store_pack<float, VE>(dw + at, narrow<float, VE>(pw));
+        store_pack<float, VE>(db + at, narrow<float, VE>(pb));
+        return;
+      }
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {   // the row's last vector: its own columns
+        if (j < own) continue;
+        dw[at + j] = fmaf(fg[j], fx[j], first ? 0.f : dw[at + j]);
+        db[at + j] = fg[j] + (first ? 0.f : db[at + j]);
+      }
+    });
   }
 }
 
