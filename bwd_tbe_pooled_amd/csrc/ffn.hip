@@ -44,7 +44,9 @@ struct Args {
 template <typename T>
 __device__ __forceinline__ void activate(int32_t act, float g, float& a, float& da) {
   if (act == TBE_ACT_SILU) {
-    const float s = 1.f / (1.f + (sizeof(T) == 4 ? expf(-g) : __expf(-g)));
+    // (16 bits: the hardware's power of two and reciprocal, 1 ulp each)
+    const float s = sizeof(T) == 4 ? 1.f / (1.f + expf(-g))
+                                   : __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * g));
     a = g * s;
     da = s * fmaf(g, 1.f - s, 1.f);
   } else {
