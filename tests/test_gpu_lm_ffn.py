@@ -153,6 +153,19 @@ FFN = [  # rows of each expert, rows of nobody, D, F, type, activation, stride p
     ([2, 1, 0, 3] * 40, 1, 64, 96, "bf16", "silu", 0),
     ([64, 31, 0, 17], 0, 1024, 712, "bf16", "silu", 0),
     ([1000], 0, 320, 1000, "bf16", "gelu", 0),
+    # few rows an expert, one to four blocks of 16 at a time, by four waves and by more
+    ([1] * 32, 0, 512, 768, "bf16", "silu", 0),
+    ([0, 1, 0, 0, 3], 0, 1030, 515, "f16", "gelu", 5),
+    ([100, 1, 0, 3] + [0] * 12, 2, 200, 136, "bf16", "silu", 0),
+    ([2, 17], 0, 96, 2056, "f32", "silu", 0),
+    ([20] * 7 + [31], 0, 264, 1024, "bf16", "silu", 0),
+    ([25], 3, 72, 80, "f16", "silu", 1),
+    ([40, 63, 0, 90], 1, 136, 2048, "bf16", "gelu", 0),
+    ([33], 0, 65, 63, "f32", "silu", 0),
+    # enough tiles of 128 x 128
+    ([70] * 30 + [1] * 5 + [200] * 5, 9, 1024, 520, "bf16", "silu", 0),
+    ([80] * 16, 0, 300, 1030, "f32", "gelu", 0),
+    ([150] * 8 + [129] * 8, 0, 1100, 1111, "f16", "silu", 0),
 ]
 
 
@@ -160,6 +173,29 @@ FFN = [  # rows of each expert, rows of nobody, D, F, type, activation, stride p
 def test_ffn(counts, tail, D, F, t, name, stride):
     say("ffn", counts if len(counts) < 8 else len(counts), tail, D, F, t, name, stride)
     check(make(gen(sum(counts) + D + F), counts, D, F, t, tail), t, name, stride, keep=D % 2 == 0)
+
+
+@pytest.mark.parametrize("t,name", [("bf16", "silu"), ("f16", "gelu")])
+def test_ffn_of_large_tiles(t, name):
+    """Products of 256 x 256 tiles, a tile's steps, rows and columns cut at every place."""
+    counts = [700, 1, 515, 0, 1030, 256, 255, 1343]
+    say("ffn large", counts, t, name)
+    check(make(gen(11), counts, 4104, 4168, t, 5), t, name)
+
+
+def test_same_bits():
+    """The same call again and again: no result depends on which workgroup comes first, and
+    nothing is read before it has arrived."""
+    for counts, D, F in (([700, 1, 515, 0, 1030, 256, 255, 1343], 4096, 4160), ([70] * 30 + [200] * 5, 1024, 520),
+                         ([9, 300], 256, 192), ([1] * 32, 512, 768)):
+        s = make(gen(sum(counts)), counts, D, F, "bf16")
+        ys, pre = forward(s, "bf16", "silu")
+        dxs, grads = backward(s, "bf16", "silu", pre)
+        for _ in range(4):
+            ys2, pre2 = forward(s, "bf16", "silu")
+            dxs2, grads2 = backward(s, "bf16", "silu", pre)
+            assert torch.equal(ys, ys2) and torch.equal(pre, pre2) and torch.equal(dxs, dxs2)
+            assert all(torch.equal(a, b) for a, b in zip(grads, grads2))
 
 
 def test_no_rows():
