@@ -116,22 +116,41 @@ __global__ __launch_bounds__(S::NT, 2) void ffn_kernel(Args g) {
   constexpr int BN = P == Up ? S::BN / 2 : S::BN, HALF = S::NF / 2, COLS = P == Up ? HALF : S::NF;
   static_assert(COLS % 2 == 0, "fragments in pairs");
   __shared__ Spans spans;
-  spans.fill<S::BM>(g.offsets, g.E, g.M);
-  const int64_t all = P == Dw ? g.tiles : (int64_t)spans.upto[g.E - 1] * g.nt;
-  const int64_t per = (all + kXcds - 1) / kXcds;
-  const int64_t begin = blockIdx.x % kXcds * per, end = begin + per < all ? begin + per : all;
-  int64_t at = begin + blockIdx.x / kXcds;
-  const int64_t stride = gridDim.x / kXcds;
+  const int64_t x = blockIdx.x % kXcds;
+  int32_t begin, end;   // this XCD's tiles
+  if constexpr (P == Dw) {
+    // an expert's tiles take as long as its rows: an XCD's experts have as many as
+    // another's (a tile's stores and first loads count as 6 steps of 64 rows)
+    spans.fill(g.offsets, g.E, g.M, [](int32_t rows) { return (rows + 63) / 64 + 6; });
+    const int64_t one = g.tiles / g.E, all = spans.upto[g.E - 1];
+    auto bound = [&](int64_t x) {
+      if (x == kXcds) return (int32_t)g.tiles;
+      const int32_t e = spans.expert_of((int32_t)(x * all / kXcds), g.E);
+      const int32_t before = e ? spans.upto[e - 1] : 0;
+      return __builtin_amdgcn_readfirstlane(
+          (int32_t)(e * one + (x * all / kXcds - before) * one / (spans.upto[e] - before)));
+    };
+    begin = bound(x);
+    end = bound(x + 1);
+  } else {
+    spans.fill(g.offsets, g.E, g.M, [](int32_t rows) { return (rows + S::BM - 1) / S::BM; });
+    const int32_t all = __builtin_amdgcn_readfirstlane(spans.upto[g.E - 1]) * g.nt;
+    const int32_t per = (all + kXcds - 1) / kXcds;
+    begin = (int32_t)x * per;
+    end = min(begin + per, all);
+  }
+  int32_t at = begin + (int32_t)(blockIdx.x / kXcds);
+  const int32_t stride = (int32_t)(gridDim.x / kXcds);
 
-  auto locate = [&](int64_t tile) {
+  auto locate = [&](int32_t tile) {
     Tile t;
     if constexpr (P == Dw) {
       // tiles of one expert: gate's, up's, down's
       const int32_t ft = (g.F + S::BM - 1) / S::BM, dt = (g.D + S::BN - 1) / S::BN;
       const int32_t dt2 = (g.D + S::BM - 1) / S::BM, ft2 = (g.F + S::BN - 1) / S::BN;
       const int32_t each = ft * dt, one = 2 * each + dt2 * ft2;
-      t.e = (int32_t)(tile / one);
-      const int32_t in = (int32_t)(tile % one);
+      t.e = tile / one;
+      const int32_t in = tile % one;
       t.which = in < each ? 0 : in < 2 * each ? 1 : 2;
       const int32_t across = t.which == 2 ? ft2 : dt, place = in - t.which * each;
       t.m0 = place / across * S::BM;
@@ -141,11 +160,11 @@ __global__ __launch_bounds__(S::NT, 2) void ffn_kernel(Args g) {
       t.first = __builtin_amdgcn_readfirstlane(spans.first[t.e]);
       t.K = __builtin_amdgcn_readfirstlane(spans.first[t.e + 1]) - t.first;
     } else {
-      t.e = __builtin_amdgcn_readfirstlane(spans.expert_of((int32_t)(tile / g.nt), g.E));
+      t.e = __builtin_amdgcn_readfirstlane(spans.expert_of(tile / g.nt, g.E));
       t.first = __builtin_amdgcn_readfirstlane(spans.first[t.e]);
       t.rows = __builtin_amdgcn_readfirstlane(spans.first[t.e + 1]);
       const int32_t blocks = (t.rows - t.first + S::BM - 1) / S::BM;
-      const int32_t place = (int32_t)tile - (__builtin_amdgcn_readfirstlane(spans.upto[t.e]) - blocks) * g.nt;
+      const int32_t place = tile - (__builtin_amdgcn_readfirstlane(spans.upto[t.e]) - blocks) * g.nt;
       // an expert's tiles in groups of 8 blocks of rows, in a group the rows first: the
       // 32 tiles that an XCD works on share rows and matrices in its L2
       constexpr int GROUP = 8;

@@ -410,11 +410,11 @@ struct Walk {
 struct Spans {
   static constexpr int kMost = 1024;
   int32_t first[kMost];   // of expert e; behind the last expert's
-  int32_t upto[kMost];    // blocks of rows of the experts up to e
+  int32_t upto[kMost];    // blocks of rows (or another number) of the experts up to e
 
-  // By every thread of the workgroup.
-  template <int BM>
-  __device__ __forceinline__ void fill(const int32_t* __restrict__ offsets, int32_t E, int32_t M) {
+  // By every thread of the workgroup. number(rows): of an expert, >= 0.
+  template <typename Number>
+  __device__ __forceinline__ void fill(const int32_t* __restrict__ offsets, int32_t E, int32_t M, Number number) {
     if (wave_index() == 0) {
       int32_t low = 0, blocks = 0;
       for (int32_t e0 = 0; e0 <= E; e0 += kWave) {
@@ -428,7 +428,7 @@ struct Spans {
         }
         a = max(a, low);
         z = max(a, z);
-        int32_t n = e < E ? (z - a + BM - 1) / BM : 0;
+        int32_t n = e < E ? number(z - a) : 0;
 #pragma unroll
         for (int d = 1; d < kWave; d <<= 1) {
           const int32_t y = __shfl_up(n, d);
@@ -446,7 +446,7 @@ struct Spans {
     __syncthreads();
   }
 
-  // The expert of block `want` of all experts': the first whose blocks reach behind it.
+  // The expert of number `want` of all experts': the first whose numbers reach behind it.
   // Found by 64 lanes in two looks. Uniform over the wave; there is one.
   __device__ __forceinline__ int32_t expert_of(int32_t want, int32_t E) const {
     const int32_t step = (E + kWave - 1) / kWave;
