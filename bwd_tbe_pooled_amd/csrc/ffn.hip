@@ -128,7 +128,8 @@ __global__ __launch_bounds__(S::NT, 2) void ffn_kernel(Args g) {
       const int32_t e = spans.expert_of((int32_t)(x * all / kXcds), g.E);
       const int32_t before = e ? spans.upto[e - 1] : 0;
       return __builtin_amdgcn_readfirstlane(
-          (int32_t)(e * one + (x * all / kXcds - before) * one / (spans.upto[e] - before)));
+          (int32_t)(e * one + (x * all - (int64_t)kXcds * before) * one /
+                                  ((int64_t)kXcds * (spans.upto[e] - before))));
     };
     begin = bound(x);
     end = bound(x + 1);
