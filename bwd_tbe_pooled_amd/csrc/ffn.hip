@@ -335,12 +335,11 @@ __global__ __launch_bounds__(S::NT, 2) void ffn_kernel(Args g) {
         if constexpr (P == Dh) asm volatile("" ::: "memory");   // this group's stores before the next loads
       }
     };
-    // stores of 16 bytes, of which a whole tile makes as many in every wave. (Dh has
-    // waited for loads made after the fetch, and so for the fetch.)
+    // stores of 16 bytes, of which a whole tile makes as many in every wave
     constexpr int STORES = S::MF * COLS / 2 * (sizeof(T) == 4 ? 2 : 1);
     if (whole) finish(std::true_type{});
     else finish(std::false_type{});
-    w.later = !whole ? 0 : P == Dh ? 48 : P == Up && g.c2 ? 3 * STORES : STORES;
+    w.later = !whole ? 0 : P == Dh || (P == Up && g.c2) ? 3 * STORES : STORES;
   }
 }
 

@@ -399,6 +399,7 @@ class AdamWState:
         if desc.bits not in (8, 32):
             raise TbeError(TBE_ERR_ARG, "AdamWState")
         self.bits = desc.bits
+        params = list(params)
         sizes = [p.numel() for p in params]
         blocks = [-(-n // ADAMW_BLOCK) for n in sizes]
         if device is None:

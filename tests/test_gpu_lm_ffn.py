@@ -175,6 +175,14 @@ def test_ffn(counts, tail, D, F, t, name, stride):
     check(make(gen(sum(counts) + D + F), counts, D, F, t, tail), t, name, stride, keep=D % 2 == 0)
 
 
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+def test_small_tiles_of_which_a_workgroup_has_several(t):
+    # 60 experts' three blocks of 64 rows by eight of columns are more than 1024 workgroups
+    counts = [129] * 60
+    say("small tiles, several", t)
+    check(make(gen(61), counts, 64, 512, t, 3), t, "silu")
+
+
 @pytest.mark.parametrize("t,name", [("bf16", "silu"), ("f16", "gelu")])
 def test_ffn_of_large_tiles(t, name):
     """Products of 256 x 256 tiles, a tile's steps, rows and columns cut at every place."""

@@ -288,3 +288,10 @@ def test_adamw_state():
         tbe.tbe_adamw_step(tbe.AdamWDesc(bits=32), params, params, s, None, None)
     with pytest.raises(TypeError, match="state: must be a device tensor"):
         tbe.tbe_adamw_step(tbe.AdamWDesc(bits=8), params, params, s, None, None)
+
+
+def test_adamw_state_of_an_iterator():
+    params = [torch.zeros(3, 5), torch.zeros(300)]
+    s = tbe.AdamWState(tbe.AdamWDesc(bits=8), (p for p in params))
+    assert [m.shape for m in s.m] == [p.shape for p in params]
+    assert s.m_flat.device == params[0].device and len(s.ms[1]) == 2
