@@ -5,7 +5,8 @@
 // of one tensor. Memory bounds it: each element of parameter, gradient and
 // moments is read once and written once, 28 bytes for float32 parameters with a
 // 16-bit gradient and copy, 10 for 16-bit parameters with 8-bit moments. A
-// thread loads all its vectors before it computes.
+// thread loads all its vectors before it computes. 357 million of the former
+// take 1.70 to 1.73 ms, 5.8 TB/s; 738 million of the latter 1.28 to 1.31, 5.7.
 //
 // An 8-bit moment's block of 256 elements lies in neighbouring lanes (64 of 4
 // elements or 32 of 8), so its scale takes one reduction and no memory.

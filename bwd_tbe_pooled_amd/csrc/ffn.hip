@@ -108,6 +108,11 @@ struct Tile {
 
 // Workgroups stay, and take tiles by XCD: each XCD has a run of neighbouring tiles,
 // its workgroups neighbours in it at any time.
+// Large batches are bound by the feeding of the matrix cores: a step of a 256 x 256 tile
+// takes 3060 to 3400 clocks, its products 2048. 131072 rows of 128 experts, 2048 x 768
+// bf16: Up 1044 TFLOP/s, Down 872, Dh 713 (its epilogue reads two values an element and
+// writes three), Dx 1067, Dw 988; 16384 rows of one expert, 4096 x 8192: 1189, 1251, 967,
+// 1303, 1305.
 template <typename T, Product P, class S, bool DIRECT>
 __global__ __launch_bounds__(S::NT, 2) void ffn_kernel(Args g) {
   __shared__ __attribute__((aligned(16))) char lds[2 * S::AREA];
@@ -347,7 +352,8 @@ __global__ __launch_bounds__(S::NT, 2) void ffn_kernel(Args g) {
 // memory's rate. A workgroup has 16 columns of an expert's products (NB = 2: of Up both
 // products', of Down 32) and up to 16 MB of its rows at a time; its waves share k. A
 // lane's pieces of a matrix row go straight to registers, and the waves' sums meet in
-// LDS. WAVES: 4, or 16 where the workgroups are too few to fill the card.
+// LDS. WAVES: 4, or 16 where the workgroups are too few to fill the card. 32 rows of 64
+// experts, 2048 x 768 bf16: Up 33 us for 167 MB of weights, 5.1 TB/s.
 template <typename T, Product P, int MB, int NB, int WAVES>
 __global__ __launch_bounds__(WAVES * kWave) void ffn_few_kernel(Args g) {
   constexpr int VE = 16 / (int)sizeof(T);
