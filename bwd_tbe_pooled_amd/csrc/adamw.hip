@@ -43,6 +43,29 @@ __device__ __forceinline__ double power(double b, uint64_t t) {
   return r;
 }
 
+// Roots of numbers >= 0, rounded to nearest. The hardware's root is off by one step now
+// and then, and takes subnormal numbers for zeros; a fused residual and one correction put
+// it right (as sqrtf does, compared for all mantissas) where no part of it is subnormal.
+template <int V>
+__device__ __forceinline__ void roots(const float (&v)[V], float (&r)[V]) {
+  uint32_t low = ~0u, high = 0;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    low = min(low, __float_as_uint(v[j]));
+    high = max(high, __float_as_uint(v[j]));
+  }
+  if (low >= __float_as_uint(0x1p-96f) && high <= __float_as_uint(0x1p96f)) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float y = __builtin_amdgcn_rsqf(v[j]), s = v[j] * y;
+      r[j] = fmaf(fmaf(-s, s, v[j]), 0.5f * y, s);
+    }
+  } else {   // (zeros among them)
+#pragma unroll
+    for (int j = 0; j < V; ++j) r[j] = sqrtf(v[j]);
+  }
+}
+
 // Largest over the LANES neighbouring lanes that hold a block, all of them active.
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_u32(uint32_t x) {
@@ -202,8 +225,18 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Args a) {
   const uint64_t n_step = step < 1 ? 1 : (uint64_t)step;
   const float b1 = (float)a.beta1, b2 = (float)a.beta2;
   const float g1 = (float)(1.0 - a.beta1), g2 = (float)(1.0 - a.beta2);
-  const float move = (float)((double)lr / (1.0 - power(a.beta1, n_step)));
-  const float unbias = (float)(1.0 / sqrt(1.0 - power(a.beta2, n_step)));
+  // The corrections of the bias, by one wave for all: in 64 bits, where 1 - beta^t keeps its
+  // digits, they cost a wave as much as 150 instructions in 32. Even lanes lr / (1 - beta1^t),
+  // odd ones 1 / sqrt(1 - beta2^t).
+  __shared__ float shared[2];
+  if (wave_index() == 0) {
+    const bool second = lane & 1;
+    const double c = 1.0 - power(second ? a.beta2 : a.beta1, n_step);
+    const float f = (float)((second ? 1.0 : (double)lr) / (second ? sqrt(c) : c));
+    if (lane < 2) shared[lane] = f;
+  }
+  __syncthreads();
+  const float move = shared[0], unbias = shared[1];
   const float keep = (float)(1.0 - (double)lr * (double)a.decay);
 
 #pragma unroll
@@ -239,15 +272,20 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Args a) {
         }
       }
     }
+    float root[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const float gj = gr[u][j] * scale;
       m[u][j] = fmaf(b1, m[u][j], g1 * gj);
       const float old = BITS == 32 ? v[u][j] : v[u][j] * v[u][j];
-      const float vn = fmaf(b2, old, g2 * gj * gj);
-      const float root = __builtin_amdgcn_sqrtf(vn);   // (1 ulp, as the reciprocal)
-      v[u][j] = BITS == 32 ? vn : root;
-      x[u][j] = fmaf(-(move * m[u][j]), __builtin_amdgcn_rcpf(fmaf(root, unbias, a.eps)), keep * x[u][j]);
+      v[u][j] = fmaf(b2, old, g2 * gj * gj);
+    }
+    roots<V>(v[u], root);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if (BITS == 8) v[u][j] = root[j];
+      // (the hardware's reciprocal is within 1 ulp)
+      x[u][j] = fmaf(-(move * m[u][j]), __builtin_amdgcn_rcpf(fmaf(root[j], unbias, a.eps)), keep * x[u][j]);
     }
     if (n == V) {
       store_pack_once<P, V>(p + i, narrow<P, V>(x[u]));
