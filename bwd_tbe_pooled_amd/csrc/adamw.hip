@@ -43,6 +43,15 @@ __device__ __forceinline__ double power(double b, uint64_t t) {
   return r;
 }
 
+// a * b + c, the product rounded before the sum. 8-bit moments have their codes at the
+// float32 formulas' borders, to the last bit: what is fused is rounded once less, and a
+// code in some millions falls to the other side.
+__device__ __forceinline__ float apart(float a, float b, float c) {
+#pragma clang fp contract(off)
+  const float p = a * b;
+  return p + c;
+}
+
 // Roots of numbers >= 0, rounded to nearest. The hardware's root is off by one step now
 // and then, and takes subnormal numbers for zeros; a fused residual and one correction put
 // it right (as sqrtf does, compared for all mantissas) where no part of it is subnormal.
@@ -100,14 +109,18 @@ __device__ __forceinline__ void decode(const Codes<V>& q, float scale, float (&f
   }
 }
 
-// Codes of f * inv; LEAST holds what is above zero at 2^-9, the smallest code, at least.
-// What is not finite becomes NaN (only asked of blocks that hold such a value).
+// Codes of f / scale, inv = 1 / scale; LEAST holds what is above zero at 2^-9, the smallest
+// code, at least. What is not finite becomes NaN (only asked of blocks that hold such a
+// value). The quotient is rounded to nearest: times the reciprocal it is off by a step or
+// two, which one residual puts right (as a division does, compared for 2^32 pairs); a code
+// at the border of two would fall to the wrong one otherwise.
 template <int V, bool LEAST, bool FINITE>
-__device__ __forceinline__ Codes<V> codes_of(const float (&f)[V], float inv) {
+__device__ __forceinline__ Codes<V> codes_of(const float (&f)[V], float scale, float inv) {
   float q[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     q[j] = f[j] * inv;
+    q[j] = fmaf(fmaf(-q[j], scale, f[j]), inv, q[j]);
     if (LEAST) q[j] = f[j] > 0.f && inv > 0.f ? fmaxf(q[j], 0x1p-9f) : q[j];
     if (!FINITE) q[j] = fabsf(f[j]) < __builtin_inff() ? q[j] : __builtin_nanf("");
   }
@@ -120,8 +133,8 @@ __device__ __forceinline__ Codes<V> codes_of(const float (&f)[V], float inv) {
   return r;
 }
 
-// f as codes and their block's scale. Rounded to nearest even, at most half a step (2^-4
-// of the value) off. Elements that do not exist are zeros. The largest magnitude is found
+// f as codes and their block's scale. A code is the nearest to its value by the scale as it
+// is stored, ties to even: at most half a step (2^-4 of the value) off. Elements that do not exist are zeros. The largest magnitude is found
 // on the bit patterns, where infinities and NaN are above all numbers: then it is looked
 // for again among the finite ones.
 template <int V, bool LEAST>
@@ -142,9 +155,10 @@ __device__ __forceinline__ Codes<V> encode(const float (&f)[V], float* scale) {
   }
   const float t = __uint_as_float(top);
   const bool some = t >= 0x1p-100f;
-  const float inv = some ? 448.f / t : 0.f;
-  *scale = some ? t * (1.f / 448.f) : 0.f;
-  return finite ? codes_of<V, LEAST, true>(f, inv) : codes_of<V, LEAST, false>(f, inv);
+  const float by = some ? t * (1.f / 448.f) : 0.f;
+  const float inv = some ? 1.f / by : 0.f;
+  *scale = by;
+  return finite ? codes_of<V, LEAST, true>(f, by, inv) : codes_of<V, LEAST, false>(f, by, inv);
 }
 
 // V elements from p + at, of which n exist (all of them in whole vectors).
@@ -276,9 +290,13 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Args a) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const float gj = gr[u][j] * scale;
-      m[u][j] = fmaf(b1, m[u][j], g1 * gj);
-      const float old = BITS == 32 ? v[u][j] : v[u][j] * v[u][j];
-      v[u][j] = fmaf(b2, old, g2 * gj * gj);
+      if constexpr (BITS == 32) {
+        m[u][j] = fmaf(b1, m[u][j], g1 * gj);
+        v[u][j] = fmaf(b2, v[u][j], g2 * gj * gj);
+      } else {
+        m[u][j] = apart(b1, m[u][j], g1 * gj);
+        v[u][j] = apart(b2, v[u][j] * v[u][j], g2 * gj * gj);
+      }
     }
     roots<V>(v[u], root);
 #pragma unroll

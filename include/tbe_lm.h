@@ -278,8 +278,12 @@ tbe_status tbe_ffn_backward(const tbe_ffn_desc* desc, const void* dys, int64_t l
  * bits = 32: m and v are float32. bits = 8: each moment is an e4m3 number (4
  * exponent and 3 mantissa bits, up to 448) times the float32 scale of its
  * block of 256 elements, counted from the tensor's start; the scale is the
- * block's largest magnitude / 448. m holds the moment, v the root of the
- * second moment; a root above zero is held as at least the smallest number, so
+ * block's largest magnitude times the float32 nearest to 1 / 448, the number
+ * the nearest to the value divided by it, ties to even. m holds the moment, v
+ * the root of the second moment, both from the formulas above with every
+ * operation rounded to float32 by itself (constants beforehand, v's second term
+ * as ((1 - beta2) g) g): they are the same bits wherever the formulas are
+ * evaluated so. A root above zero is held as at least the smallest number, so
  * that no update is divided by eps alone. Blocks whose largest magnitude is
  * below 2^-100 are held as zeros, a moment that is not finite as NaN (its
  * block's others keep theirs). All buffers zero is the state before step 1. */
