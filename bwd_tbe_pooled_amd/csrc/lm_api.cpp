@@ -2,6 +2,7 @@
 // any launch, then the launchers on the caller's stream.
 #include <algorithm>
 #include <cmath>
+#include <limits>
 #include <new>
 
 #include "lm.h"
@@ -82,6 +83,8 @@ tbe_status check(const tbe_adamw_desc* d) {
   if (!(d->eps >= 0) || !std::isfinite((float)d->eps)) return TBE_ERR_ARG;
   if (!(d->weight_decay >= 0) || !std::isfinite((float)d->weight_decay)) return TBE_ERR_ARG;
   if (!type_ok(d->pdtype) || !type_ok(d->gdtype)) return TBE_ERR_UNSUPPORTED;
+  // the kernel's reciprocal takes subnormal numbers for zeros, and 0 / eps would be NaN
+  if (d->eps > 0 && (float)d->eps < std::numeric_limits<float>::min()) return TBE_ERR_UNSUPPORTED;
   if (d->cdtype != -1 && (d->pdtype != TBE_F32 || (d->cdtype != TBE_F16 && d->cdtype != TBE_BF16)))
     return TBE_ERR_UNSUPPORTED;
   return TBE_OK;

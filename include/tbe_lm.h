@@ -293,7 +293,8 @@ typedef struct {
     int32_t cdtype;       /* of the copies: TBE_F16 or TBE_BF16 with float32 parameters, -1: none */
     int32_t bits;         /* 32 or 8 */
     double beta1, beta2;  /* in [0, 1) */
-    double eps;           /* >= 0, finite */
+    double eps;           /* >= 0, finite; TBE_ERR_UNSUPPORTED above 0 and below 2^-126.
+                             With eps 0 an element whose gradients are all zero gives NaN. */
     double weight_decay;  /* >= 0, finite */
 } tbe_adamw_desc;
 
