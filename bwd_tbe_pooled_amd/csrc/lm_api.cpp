@@ -62,11 +62,13 @@ size_t norm_bytes(const tbe_norm_desc& d) {
 }
 
 constexpr int64_t kFfnElems = int64_t(1) << 36;
+// Rows: the kernels count a tile's rows, up to 256, from its first one in 32 bits.
+constexpr int64_t kFfnRows = kI32Lim - 1024;
 tbe_status check(const tbe_ffn_desc* d) {
   if (!d || d->M < 0 || d->E < 1 || d->D < 1 || d->F < 1) return TBE_ERR_ARG;
   if (d->act != TBE_ACT_SILU && d->act != TBE_ACT_GELU) return TBE_ERR_ARG;
   if (!type_ok(d->dtype)) return TBE_ERR_UNSUPPORTED;
-  if (d->M >= kI32Lim || d->E > 1023 || d->D > 65536 || d->F > 65536) return TBE_ERR_UNSUPPORTED;
+  if (d->M > kFfnRows || d->E > 1023 || d->D > 65536 || d->F > 65536) return TBE_ERR_UNSUPPORTED;
   if (d->M * std::max(d->D, 2 * d->F) > kFfnElems) return TBE_ERR_UNSUPPORTED;
   return (int64_t)d->E * d->D * d->F > kFfnElems ? TBE_ERR_UNSUPPORTED : TBE_OK;
 }

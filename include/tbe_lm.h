@@ -224,7 +224,7 @@ tbe_status tbe_norm_backward(const tbe_norm_desc* desc, const void* dy, int64_t 
  * Products accumulate in float32. In 16-bit types pre, h and the gradients of
  * g and u are rounded to the type between the products that use them.
  * 1 <= E <= 1023, 1 <= D, F <= 65536, M * max(D, 2 F) <= 2^36,
- * E * D * F <= 2^36, M < 2^31 - 1. */
+ * E * D * F <= 2^36, M < 2^31 - 1024. */
 typedef enum { TBE_ACT_SILU = 0, TBE_ACT_GELU = 1 } tbe_act;   /* GELU by the error function */
 
 typedef struct {
