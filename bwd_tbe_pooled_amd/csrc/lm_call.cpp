@@ -382,7 +382,8 @@ tbe_stack stack(PyObject* o, const char* name, at::ScalarType t, int64_t E, int6
   if (stride[2] != 1 && cols > 1) refuse(name, "columns must be contiguous");
   const int64_t ld = rows <= 1 ? cols : stride[1];
   const int64_t each = E <= 1 ? rows * ld : stride[0];
-  if (out && (ld < cols || each / ld < rows)) refuse(name, "rows of an output must not overlap");
+  // (rows without columns are the library's to refuse)
+  if (out && cols > 0 && (ld < cols || each / ld < rows)) refuse(name, "rows of an output must not overlap");
   return {x.data_ptr(), ld, each};
 }
 

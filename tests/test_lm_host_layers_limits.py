@@ -1,8 +1,12 @@
 """Layer norm, experts' feed-forward and AdamW: limits and refusals that need no GPU, at the
 values next to them."""
 import ctypes
+import types
+import warnings
 
 import pytest
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
 
 tbe = pytest.importorskip("bwd_tbe_pooled_amd", reason="libtbe.so not built")
 from tests.test_lm_host_layers import OK, UNSUP, adamw, calls, ffn, lm, status, step  # noqa: E402
@@ -25,3 +29,25 @@ def test_ffn_rows_leave_room_for_a_tile():
         d = ffn(M=M, D=8, F=8)
         for f, args, *_ in calls(d):
             assert status(f, d, args) == UNSUP, f.__name__
+
+
+@pytest.mark.parametrize("D,F", [(0, 1), (1, 0), (0, 0), (0, 5), (5, 0)])
+def test_matrices_without_columns_are_refused(D, F):
+    """By the description's check, after the tensors': their rows' strides may be zero."""
+    M, E = 3, 1
+    d = tbe.FfnDesc(M, E, D, F)
+    with FakeTensorMode(), warnings.catch_warnings():
+        warnings.simplefilter("ignore")   # torch's on the address of a tensor without memory
+
+        def new(*shape, dtype=torch.bfloat16):
+            return torch.empty(shape, dtype=dtype, device="cuda:0")
+        x, pre, offsets = new(M, D), new(M, 2 * F), new(E + 1, dtype=torch.int32)
+        ws = new(1 << 20, dtype=torch.uint8)
+        gate, down = new(E, F, D), new(E, D, F)
+        stream = types.SimpleNamespace(cuda_stream=64, device_index=0)
+        for w in (gate, gate.as_strided(gate.shape, (0, 0, 1))):
+            with pytest.raises((tbe.TbeError, TypeError)):
+                tbe.tbe_ffn_backward(d, x, x, offsets, gate, gate, down, pre, x, w, w, down, ws, stream)
+        with pytest.raises(tbe.TbeError) as e:
+            tbe.tbe_ffn_forward(d, x, offsets, gate, gate, down, pre, x, ws, stream)
+        assert e.value.status == tbe.TBE_ERR_ARG
