@@ -456,32 +456,54 @@ void* dense(PyObject* o, const char* name, at::ScalarType t, int64_t n) {
   return x.data_ptr();
 }
 
-// adamw_step(desc, table, state, params, grads, step, lr, scale, copies, stream): `table`
-// is the state's array of tbe_adamw_tensor with the moments filled in, `state` one of
-// their buffers; the call fills in the rest.
-PyObject* adamw_step(PyObject*, Args args, Py_ssize_t n) {
-  return call<10>(args, n, [](Args a) {
-    const auto& d = desc<tbe_adamw_desc>(a[0]);
-    if (!PyTuple_Check(a[1]) || PyTuple_GET_SIZE(a[1]) != 2) refuse("state", "expected an AdamWState");
-    auto* t = static_cast<tbe_adamw_tensor*>(PyLong_AsVoidPtr(PyTuple_GET_ITEM(a[1], 0)));
-    const Py_ssize_t count = PyLong_AsSsize_t(PyTuple_GET_ITEM(a[1], 1));
+// The state's array of tbe_adamw_tensor with the moments filled in: `table` is its address,
+// its length, the moments' buffers and the addresses these had when it was filled.
+struct Table {
+  tbe_adamw_tensor* t;
+  Py_ssize_t count;
+  Table(PyObject* o, const tbe_adamw_desc& d) {
+    if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 4) refuse("state", "expected an AdamWState");
+    t = static_cast<tbe_adamw_tensor*>(PyLong_AsVoidPtr(PyTuple_GET_ITEM(o, 0)));
+    count = PyLong_AsSsize_t(PyTuple_GET_ITEM(o, 1));
+    PyObject *flats = PyTuple_GET_ITEM(o, 2), *at = PyTuple_GET_ITEM(o, 3);
+    const Py_ssize_t kinds = d.bits == 32 ? 2 : 4;
+    if (!PyTuple_Check(flats) || !PyTuple_Check(at) || PyTuple_GET_SIZE(flats) != kinds ||
+        PyTuple_GET_SIZE(at) != kinds)
+      refuse("state", "expected an AdamWState of the description's bits");
+    for (Py_ssize_t i = 0; i < kinds; ++i) {
+      PyObject* const f = PyTuple_GET_ITEM(flats, i);
+      if (!THPVariable_Check(f) || THPVariable_Unpack(f).data_ptr() != PyLong_AsVoidPtr(PyTuple_GET_ITEM(at, i)))
+        refuse("state", "its buffers are not where they were when it was made");
+    }
     if (PyErr_Occurred()) throw Refused{};
-    tensor(a[2], "state", d.bits == 32 ? at::kFloat : at::kFloat8_e4m3fn);
-    const List params(a[3], "params", count), grads(a[4], "grads", count);
+    for (Py_ssize_t i = 0; i < kinds; ++i)
+      tensor(PyTuple_GET_ITEM(flats, i), "state", i < 2 && d.bits == 8 ? at::kFloat8_e4m3fn : at::kFloat);
+  }
+};
+
+// adamw_step(desc, table, params, grads, step, lr, scale, copies, stream): the call fills
+// in what the state's table lacks.
+PyObject* adamw_step(PyObject*, Args args, Py_ssize_t n) {
+  return call<9>(args, n, [](Args a) {
+    const auto& d = desc<tbe_adamw_desc>(a[0]);
+    const Table table(a[1], d);
+    tbe_adamw_tensor* const t = table.t;
+    const Py_ssize_t count = table.count;
+    const List params(a[2], "params", count), grads(a[3], "grads", count);
     const bool copy = d.cdtype >= 0;
-    if (copy == (a[8] == Py_None))
+    if (copy == (a[7] == Py_None))
       refuse("copies", copy ? "expected a list or tuple of tensors" : "the description has none");
-    PyObject** const copies = copy ? List(a[8], "copies", count).item : nullptr;
+    PyObject** const copies = copy ? List(a[7], "copies", count).item : nullptr;
     for (Py_ssize_t i = 0; i < count; ++i) {
       t[i].p = dense(params.item[i], "params", type_of(d.pdtype), t[i].n);
       t[i].g = dense(grads.item[i], "grads", type_of(d.gdtype), t[i].n);
       t[i].c = copy ? dense(copies[i], "copies", type_of((tbe_dtype)d.cdtype), t[i].n) : nullptr;
     }
-    auto* step = static_cast<const int64_t*>(vec(a[5], "step", at::kLong, 1));
-    auto* lr = static_cast<const float*>(vec(a[6], "lr", at::kFloat, 1));
-    auto* scale = a[7] == Py_None ? nullptr
-                                  : static_cast<const float*>(vec(a[7], "scale", at::kFloat, 1));
-    return lib.adamw_step(&d, t, count, step, lr, scale, stream_of(a[9]));
+    auto* step = static_cast<const int64_t*>(vec(a[4], "step", at::kLong, 1));
+    auto* lr = static_cast<const float*>(vec(a[5], "lr", at::kFloat, 1));
+    auto* scale = a[6] == Py_None ? nullptr
+                                  : static_cast<const float*>(vec(a[6], "scale", at::kFloat, 1));
+    return lib.adamw_step(&d, t, count, step, lr, scale, stream_of(a[8]));
   });
 }
 

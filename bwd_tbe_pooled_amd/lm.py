@@ -392,7 +392,9 @@ class AdamWDesc(_LmDesc):
 class AdamWState:
     """The moments of `params`, zero before the first step: `m` and `v` of each tensor, and
     with 8 bits the scales `ms` and `vs` of their blocks (v's numbers are roots). Each kind
-    is one buffer (`m_flat` ...) in which tensors begin at whole blocks."""
+    is one buffer (`m_flat` ...) in which tensors begin at whole blocks. The step writes
+    through addresses taken here: saved moments are copied in (`state.m_flat.copy_(...)`),
+    other tensors cannot be put in the buffers' place."""
 
     def __init__(self, desc: AdamWDesc, params, device=None):
         _need_desc(desc, AdamWDesc)
@@ -409,25 +411,36 @@ class AdamWState:
         # zeros are written as bytes: e4m3 has no fill
         self.m_flat, self.v_flat = (torch.zeros(total * ADAMW_BLOCK * bytes_of, dtype=torch.uint8,
                                                 device=device).view(kind) for _ in "mv")
-        self.m, self.v, self.ms, self.vs = [], [], None, None
+        m, v, ms, vs = [], [], [], []
+        flats = (self.m_flat, self.v_flat)
         if desc.bits == 8:
             self.ms_flat, self.vs_flat = (torch.zeros(total, device=device) for _ in "mv")
-            self.ms, self.vs = [], []
+            flats += (self.ms_flat, self.vs_flat)
         self._c = (tbe_adamw_tensor * max(1, len(sizes)))()
         at = 0
         for i, (p, n, b) in enumerate(zip(params, sizes, blocks)):
             a = at * ADAMW_BLOCK
-            self.m.append(self.m_flat[a:a + n].view(p.shape))
-            self.v.append(self.v_flat[a:a + n].view(p.shape))
+            m.append(self.m_flat[a:a + n].view(p.shape))
+            v.append(self.v_flat[a:a + n].view(p.shape))
             self._c[i].n = n
             self._c[i].m, self._c[i].v = (f.data_ptr() + a * bytes_of for f in (self.m_flat, self.v_flat))
             if desc.bits == 8:
-                self.ms.append(self.ms_flat[at:at + b])
-                self.vs.append(self.vs_flat[at:at + b])
+                ms.append(self.ms_flat[at:at + b])
+                vs.append(self.vs_flat[at:at + b])
                 self._c[i].mscale, self._c[i].vscale = (f.data_ptr() + 4 * at
                                                         for f in (self.ms_flat, self.vs_flat))
             at += b
-        self._table = (ctypes.addressof(self._c), len(sizes))
+        self.m, self.v = tuple(m), tuple(v)
+        self.ms, self.vs = (tuple(ms), tuple(vs)) if desc.bits == 8 else (None, None)
+        self._table = (ctypes.addressof(self._c), len(sizes), flats, tuple(f.data_ptr() for f in flats))
+
+    def __setattr__(self, name, value):
+        if "_table" in self.__dict__:
+            raise AttributeError(f"AdamWState: {name} stays what it is; copy into the buffers")
+        object.__setattr__(self, name, value)
+
+    def __delattr__(self, name):
+        raise AttributeError(f"AdamWState: {name} stays what it is")
 
 
 def tbe_adamw_step(desc: AdamWDesc, params, grads, state: AdamWState, step, lr, scale=None, copies=None,
@@ -439,7 +452,6 @@ def tbe_adamw_step(desc: AdamWDesc, params, grads, state: AdamWState, step, lr, 
         _need_desc(desc, AdamWDesc)
     if not isinstance(state, AdamWState) or state.bits != desc.bits:
         raise TypeError("state: expected an AdamWState of the description's bits")
-    status = _lmcall.adamw_step(desc.ref, state._table, state.m_flat, params, grads, step, lr, scale,
-                                copies, stream)
+    status = _lmcall.adamw_step(desc.ref, state._table, params, grads, step, lr, scale, copies, stream)
     if status:
         raise TbeError(status, "tbe_adamw_step")
