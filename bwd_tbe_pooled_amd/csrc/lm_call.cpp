@@ -456,6 +456,15 @@ void* dense(PyObject* o, const char* name, at::ScalarType t, int64_t n) {
   return x.data_ptr();
 }
 
+// The same for what goes with a parameter: of its shape, or one of the two is flat and
+// memory's order says which element is which.
+void* beside(PyObject* o, const char* name, at::ScalarType t, PyObject* param, int64_t n) {
+  void* const p = dense(o, name, t, n);
+  const at::Tensor &x = THPVariable_Unpack(o), &y = THPVariable_Unpack(param);
+  if (x.sizes() != y.sizes() && x.dim() != 1 && y.dim() != 1) refuse(name, "expected its parameter's shape");
+  return p;
+}
+
 // The state's array of tbe_adamw_tensor with the moments filled in: `table` is its address,
 // its length, the moments' buffers and the addresses these had when it was filled.
 struct Table {
@@ -496,8 +505,8 @@ PyObject* adamw_step(PyObject*, Args args, Py_ssize_t n) {
     PyObject** const copies = copy ? List(a[7], "copies", count).item : nullptr;
     for (Py_ssize_t i = 0; i < count; ++i) {
       t[i].p = dense(params.item[i], "params", type_of(d.pdtype), t[i].n);
-      t[i].g = dense(grads.item[i], "grads", type_of(d.gdtype), t[i].n);
-      t[i].c = copy ? dense(copies[i], "copies", type_of((tbe_dtype)d.cdtype), t[i].n) : nullptr;
+      t[i].g = beside(grads.item[i], "grads", type_of(d.gdtype), params.item[i], t[i].n);
+      t[i].c = copy ? beside(copies[i], "copies", type_of((tbe_dtype)d.cdtype), params.item[i], t[i].n) : nullptr;
     }
     auto* step = static_cast<const int64_t*>(vec(a[4], "step", at::kLong, 1));
     auto* lr = static_cast<const float*>(vec(a[5], "lr", at::kFloat, 1));

@@ -447,7 +447,8 @@ def tbe_adamw_step(desc: AdamWDesc, params, grads, state: AdamWState, step, lr, 
                    stream=None):
     """One step over the lists `params` and `grads`. step (int64 [1], counted from 1), lr and
     scale (float32 [1]; scale multiplies the gradients, None for 1) are device tensors; copies:
-    a list of tensors that take the new parameters in 16 bits."""
+    a list of tensors that take the new parameters in 16 bits. Gradients and copies have their
+    parameter's shape, or either of the two is flat."""
     if type(desc) is not AdamWDesc:
         _need_desc(desc, AdamWDesc)
     if not isinstance(state, AdamWState) or state.bits != desc.bits:
