@@ -40,6 +40,28 @@ struct Args {
   tbe_stack o0, o1, o2;
 };
 
+// exp(-g^2 / 2) and the normal distribution up to g. Far below zero 1 + erf cancels: the
+// complement is formed there. 16 bits: it is the exponential times a polynomial in
+// t = 1 / (1 + 0.46 |g| / sqrt(2)), the one of 8 terms with the least largest relative
+// error, 2^-20; 2^-17 at -13 with the exponent's rounding.
+template <typename T>
+__device__ __forceinline__ void normal(float g, float& e, float& cdf) {
+  if constexpr (sizeof(T) == 4) {
+    e = expf(-0.5f * g * g);
+    cdf = 0.5f * erfcf(g * -0.70710678f);
+  } else {
+    e = __builtin_amdgcn_exp2f(g * g * -0.72134752f);
+    const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(g), 0.325052302f, 1.f));
+    constexpr float k[8] = {0.129676998f, 0.129694268f, 0.115500562f, 0.0936133787f,
+                            0.0257740766f, 0.085640423f, -0.113822207f, 0.0339228176f};
+    float p = k[7];
+#pragma unroll
+    for (int i = 6; i >= 0; --i) p = fmaf(p, t, k[i]);
+    p *= t * e;
+    cdf = g < 0.f ? p : 1.f - p;
+  }
+}
+
 // The activation and its derivative.
 template <typename T>
 __device__ __forceinline__ void activate(int32_t act, float g, float& a, float& da) {
@@ -50,9 +72,10 @@ __device__ __forceinline__ void activate(int32_t act, float g, float& a, float& 
     a = g * s;
     da = s * fmaf(g, 1.f - s, 1.f);
   } else {
-    const float cdf = 0.5f * (1.f + erff(g * 0.70710678f));
+    float e, cdf;
+    normal<T>(g, e, cdf);
     a = g * cdf;
-    da = fmaf(g * 0.39894228f, sizeof(T) == 4 ? expf(-0.5f * g * g) : __expf(-0.5f * g * g), cdf);
+    da = fmaf(g * 0.39894228f, e, cdf);
   }
 }
 
