@@ -138,7 +138,7 @@ struct Tile {
 // 1303, 1305.
 template <typename T, Product P, class S, bool DIRECT>
 __global__ __launch_bounds__(S::NT, 2) void ffn_kernel(Args g) {
-  __shared__ __attribute__((aligned(16))) char lds[2 * S::AREA];
+  __shared__ __attribute__((aligned(kLdsUnit))) char lds[2 * S::AREA];
   constexpr int BK = kStepBytes / (int)sizeof(T);
   // columns of a tile: of Up's two products half each
   constexpr int BN = P == Up ? S::BN / 2 : S::BN, HALF = S::NF / 2, COLS = P == Up ? HALF : S::NF;

@@ -21,6 +21,9 @@ namespace tbe {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kStepBytes = 128;   // of k in one step
+// Every operand's area in LDS begins at a multiple of the longest row of Across: frag()
+// finds columns by exclusive or with whole addresses.
+constexpr int kLdsUnit = 512;
 
 template <typename T> struct Mma;
 template <> struct Mma<bf16_t> {
@@ -97,6 +100,7 @@ struct Operand {
   static constexpr int PIECES = ROWS * (kStepBytes / 16) / NT;
   static constexpr int READS = L == Along ? 1 : sizeof(T) == 2 ? 2 : 4;   // of LDS, for a fragment
   static_assert(PIECES * NT * 16 == ROWS * kStepBytes, "whole pieces per thread");
+  static_assert(L == Along || (kLdsUnit % BYTES == 0 && (ROWS * kStepBytes) % kLdsUnit == 0), "areas of whole rows");
   int32_t limit;     // Across: columns behind the tile's start
   int32_t left;      // elements of k not loaded yet
   int64_t step;      // elements from one step to the next
@@ -236,7 +240,7 @@ struct Operand {
       typedef __attribute__((address_space(3))) const u32x4* ptr;
       return __builtin_bit_cast(uint4, *(ptr)(uintptr_t)(at + row * kStepBytes));
     } else {
-      at ^= row * (int)sizeof(T);   // (units are permuted by the same pattern in all columns)
+      at ^= row * (int)sizeof(T);   // (units are permuted by the same pattern in all columns; kLdsUnit)
       if constexpr (sizeof(T) == 2) {
         typedef short s16x4 __attribute__((ext_vector_type(4)));
         typedef __attribute__((address_space(3))) s16x4* ptr;
@@ -259,6 +263,7 @@ struct Shape {
   static constexpr int WM = WM_, WN = WN_, MF = MF_, NF = NF_;
   static constexpr int BM = WM * MF * 16, BN = WN * NF * 16, NT = WM * WN * kWave;
   static constexpr int AREA = (BM + BN) * kStepBytes;   // of LDS for one step
+  static_assert(BM * kStepBytes % kLdsUnit == 0 && AREA % kLdsUnit == 0, "operands' areas at whole units");
 };
 
 // A wave's fragments of half a step.
