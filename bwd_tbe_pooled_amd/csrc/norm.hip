@@ -447,33 +447,37 @@ __global__ __launch_bounds__(kThreads) void norm_wide_backward_kernel(BackwardAr
 }
 
 // dw[d], db[d]: the partials of column d added by 64 lanes, then by a fixed tree.
-// A workgroup has 16 columns: 64-byte pieces of the partial rows, and enough
+// A workgroup takes 16 columns at a time: 64-byte pieces of the partial rows, and enough
 // workgroups for the narrowest rows.
+constexpr int64_t kJoinBlocks = 1 << 16;   // at most: a launch has less than 2^32 threads
 __global__ __launch_bounds__(kThreads) void norm_join_kernel(const float* parts, int32_t P,
                                                              int32_t D, int32_t wtype, void* dw,
                                                              void* db) {
   __shared__ float meet[64][17];
   const int32_t col = threadIdx.x % 16, lane = threadIdx.x / 16;
-  const int64_t i = (int64_t)blockIdx.x * 16 + col;   // of 2 D columns: dw's, then db's
-  float s = 0.f;
-  if (i < 2 * (int64_t)D) {
+  const int64_t columns = 2 * (int64_t)D;   // dw's, then db's
+  for (int64_t i0 = (int64_t)blockIdx.x * 16; i0 < columns; i0 += (int64_t)gridDim.x * 16) {
+    const int64_t i = i0 + col;
+    float s = 0.f;
+    if (i < columns) {
 #pragma unroll 4
-    for (int32_t p = lane; p < P; p += 64) s += parts[(int64_t)p * 2 * D + i];
-  }
-  meet[lane][col] = s;
-  __syncthreads();
-  for (int half = 32; half > 0; half /= 2) {
-    if (lane < half) meet[lane][col] += meet[lane + half][col];
+      for (int32_t p = lane; p < P; p += 64) s += parts[(int64_t)p * columns + i];
+    }
+    meet[lane][col] = s;
     __syncthreads();
+    for (int half = 32; half > 0; half /= 2) {
+      if (lane < half) meet[lane][col] += meet[lane + half][col];
+      __syncthreads();
+    }
+    void* out = i < D ? dw : db;
+    if (lane == 0 && i < columns && out) {
+      const int64_t d = i < D ? i : i - D;
+      const float v = meet[0][col];   // (the next columns' are written to it by this lane)
+      if (wtype == TBE_F32) static_cast<float*>(out)[d] = v;
+      else if (wtype == TBE_F16) static_cast<f16_t*>(out)[d] = round_to<f16_t>(v);
+      else static_cast<bf16_t*>(out)[d] = round_to<bf16_t>(v);
+    }
   }
-  if (lane > 0 || i >= 2 * (int64_t)D) return;
-  void* out = i < D ? dw : db;
-  if (!out) return;
-  const int64_t d = i < D ? i : i - D;
-  const float v = meet[0][col];
-  if (wtype == TBE_F32) static_cast<float*>(out)[d] = v;
-  else if (wtype == TBE_F16) static_cast<f16_t*>(out)[d] = round_to<f16_t>(v);
-  else static_cast<bf16_t*>(out)[d] = round_to<bf16_t>(v);
 }
 
 // Calls f(VE, LPR, NV) with the shape for rows of D columns: one vector a lane as long
@@ -557,8 +561,9 @@ hipError_t launch_norm_backward(const tbe_norm_desc& d, const void* dy, int64_t 
     });
   }
   if (e != hipSuccess || !sums) return e;
-  norm_join_kernel<<<(unsigned)((2 * (int64_t)d.D + 15) / 16), kThreads, 0, s>>>(
-      parts, P, d.D, (int32_t)d.wdtype, dw, db);
+  const int64_t joins = std::min<int64_t>((2 * (int64_t)d.D + 15) / 16, kJoinBlocks);
+  norm_join_kernel<<<(unsigned)joins, kThreads, 0, s>>>(parts, P, d.D, (int32_t)d.wdtype,
+                                                        dw, db);
   return hipGetLastError();
 }
 
