@@ -6,7 +6,9 @@
 // moments is read once and written once, 28 bytes for float32 parameters with a
 // 16-bit gradient and copy, 10 for 16-bit parameters with 8-bit moments. A
 // thread loads all its vectors before it computes. 357 million of the former
-// take 1.70 to 1.73 ms, 5.8 TB/s; 738 million of the latter 1.28 to 1.31, 5.7.
+// take 1.73 to 1.75 ms, 5.8 TB/s; 738 million of the latter 1.29 to 1.30, 5.7.
+// (The latter's 57 vector instructions an element take 1.06 ms to issue: exact
+// roots and quotients are paid for by what one wave works out for four.)
 //
 // An 8-bit moment's block of 256 elements lies in neighbouring lanes (64 of 4
 // elements or 32 of 8), so its scale takes one reduction and no memory.
@@ -134,9 +136,9 @@ __device__ __forceinline__ Codes<V> codes_of(const float (&f)[V], float scale, f
 }
 
 // f as codes and their block's scale. A code is the nearest to its value by the scale as it
-// is stored, ties to even: at most half a step (2^-4 of the value) off. Elements that do not exist are zeros. The largest magnitude is found
-// on the bit patterns, where infinities and NaN are above all numbers: then it is looked
-// for again among the finite ones.
+// is stored, ties to even: at most half a step (2^-4 of the value) off. Elements that do not
+// exist are zeros. The largest magnitude is found on the bit patterns, where infinities and
+// NaN are above all numbers: then it is looked for again among the finite ones.
 template <int V, bool LEAST>
 __device__ __forceinline__ Codes<V> encode(const float (&f)[V], float* scale) {
   uint32_t top = 0;

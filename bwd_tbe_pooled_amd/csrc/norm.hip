@@ -14,8 +14,10 @@
 // them in a fixed order. Rows wider than 2048 vectors are read again for each
 // pass (norm_wide_*).
 //
-// 16384 rows of 4096 bf16: forward 50 to 54 us, 5.0 to 5.4 TB/s; backward 75 to 87, 4.6 to
-// 5.4, and the join of 256 partial rows 5. 262144 rows of 1024: backward 261 us, 6.2 TB/s.
+// Medians of many launches: 16384 rows of 4096 bf16, forward 54 us, 5.0 TB/s, backward 85,
+// 4.8, and the join of 256 partial rows 5; 262144 rows of 1024, backward 272 us, 5.9 TB/s
+// (the least of them 50, 73 and 261). Launches 8 to 50 after a pause of the card take up to
+// a third more, on any buffers, and then as long as the first; a copy's do not. Not found why.
 #include <algorithm>
 #include <type_traits>
 

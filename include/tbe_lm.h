@@ -299,8 +299,8 @@ typedef struct {
 } tbe_adamw_desc;
 
 /* One tensor of n elements, dense, any start (8-bit moments: a multiple of 8
- * bytes). Nothing that is written may overlap; a parameter or a copy that
- * overlaps another one is refused. */
+ * bytes). Nothing that is written may overlap; a parameter that overlaps
+ * another parameter, or a copy another copy, is refused. */
 typedef struct {
     void* p;              /* parameters, updated */
     const void* g;        /* gradients */
